@@ -54,7 +54,9 @@ typedef enum {
   H3KV_ERR_INVALID_ARG = 1,    /* null/misaligned pointer, bad size or chunk  */
   H3KV_ERR_UNSUPPORTED = 2,    /* head_dim != 128, or device is not sm_103   */
   H3KV_ERR_CUDA = 3,           /* a CUDA runtime call or launch failed       */
-  H3KV_ERR_DEVICE_TIMEOUT = 4  /* a bounded in-kernel wait ran out           */
+  H3KV_ERR_DEVICE_TIMEOUT = 4, /* a bounded in-kernel wait ran out           */
+  H3KV_ERR_DEVICE_DATA = 5     /* an index array in device memory held a
+                                  value out of range (h3kv_serve.h)          */
 } h3kv_status;
 
 /* The kvi8r store: for K and for V, int8 codes [heads, seq, 128] and fp16

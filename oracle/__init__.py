@@ -1,4 +1,4 @@
-"""fp64 CPU oracle for the kvi8r, kvf8s and kvfp4 stores and attention (test
+"""fp64 CPU oracle for the kvi8r, kvf8s and kvfp4 stores, their attention and the serving operators (test
 infrastructure only).
 
 Only the test suite, ``__graft_entry__.smoke()`` and ``bench.py``'s CPU
@@ -12,3 +12,4 @@ from .kvi8r import (  # noqa: F401
 )
 from . import kvf8s  # noqa: F401
 from . import kvfp4  # noqa: F401
+from . import serve  # noqa: F401

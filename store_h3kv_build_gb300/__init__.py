@@ -6,4 +6,4 @@ over it; importing the binding loads the library and raises if it has not been
 built.  This package ``__init__`` imports nothing heavy so that the input
 generator (``synth``) can be used without the library.
 """
-__all__ = ["binding", "synth"]
+__all__ = ["binding", "paging", "synth"]

@@ -29,6 +29,9 @@ H3KV_ERR_INVALID_ARG = 1
 H3KV_ERR_UNSUPPORTED = 2
 H3KV_ERR_CUDA = 3
 H3KV_ERR_DEVICE_TIMEOUT = 4
+H3KV_ERR_DEVICE_DATA = 5
+PAGE_SIZES = (16, 32, 64, 128)
+TREE_MAX_NODES = 64
 
 
 class h3kv_store(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
@@ -69,7 +72,29 @@ class h3kv_store_fp4(ctypes.Structure):  # noqa: N801 - mirrors the C struct nam
     ]
 
 
+class h3kv_rows(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("head_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
+class h3kv_paged_store(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("pages", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+    ]
+
+
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_rows, _paged = ctypes.POINTER(h3kv_rows), ctypes.POINTER(h3kv_paged_store)
 _SIGS = {
     "h3kv_abi_version": (ctypes.c_uint32, []),
     "h3kv_store_bytes": (ctypes.c_size_t, [_i32, _i64, _i32]),
@@ -98,6 +123,16 @@ _SIGS = {
     "h3kv_attend_launch_count": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]),
     "h3kv_debug_withhold_p": (ctypes.c_int, [ctypes.c_int32]),
     "h3kv_strerror": (ctypes.c_char_p, [ctypes.c_int]),
+    "h3kv_paged_store_bytes": (ctypes.c_size_t, [_i32, _i32, _i32, _i32]),
+    "h3kv_paged_append": (ctypes.c_int, [_rows, _rows, _vp, _i64, _paged, _vp]),
+    "h3kv_paged_read": (ctypes.c_int, [_paged, _vp, _i64, _rows, _rows, _vp]),
+    "h3kv_paged_copy": (ctypes.c_int, [_paged, _vp, _vp, _i64, _vp]),
+    "h3kv_paged_keep": (ctypes.c_int, [_paged, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp]),
+    "h3kv_attend_tree_workspace_bytes": (ctypes.c_size_t, [_i32, _i32, _i64, _i32]),
+    "h3kv_attend_tree": (ctypes.c_int, [_rows, _i32, _i64, _paged, _vp, _i64, _vp, _vp, _i32, _vp, _f32, _rows, _vp,
+                                        _vp, ctypes.c_size_t, _vp]),
+    "h3kv_attend_prompt": (ctypes.c_int, [_rows, _i32, _i64, _rows, _rows, _i32, _i64, _vp, _vp, _i32, _i32, _f32,
+                                          _rows, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -448,6 +483,271 @@ def attend_fp4(Q: torch.Tensor, store: StoreFp4, q_chunk: int = 16384, kv_block:
     return out
 
 
+# ------------------------------------------------------- serving operators --
+def _need_strided(t, name: str, heads: int | None = None, rows: int | None = None) -> h3kv_rows:
+    """bf16 [heads, rows, 128] whose 128 values are contiguous; heads and rows
+    may lie at any stride that is a multiple of 8 elements (a projection's
+    output [rows, heads, 128] is passed as its transpose(0, 1))."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [heads, rows, {HEAD_DIM}]")
+    if heads is not None and t.shape[0] != heads:
+        raise ValueError(f"{name}: {t.shape[0]} heads, expected {heads}")
+    if rows is not None and t.shape[1] != rows:
+        raise ValueError(f"{name}: {t.shape[1]} rows, expected {rows}")
+    if t.numel():
+        if t.stride(2) != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        for d in (0, 1):
+            if t.shape[d] > 1 and (t.stride(d) % 8 != 0 or t.stride(d) < HEAD_DIM):
+                raise ValueError(f"{name}: stride {t.stride(d)} of dimension {d} must be a multiple of 8, "
+                                 f"at least {HEAD_DIM}")
+        if t.data_ptr() % 16 != 0:
+            raise ValueError(f"{name}: must be 16-byte aligned")
+    # the stride of a dimension of one entry is never used
+    return h3kv_rows(_ptr(t), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _need_index(t, name: str, shape=None) -> None:
+    _need(t, name, torch.int32, shape)
+
+
+def _need_apart(out, **inputs) -> None:
+    """An output may not share memory with an input that other CTAs still
+    read; tensors of one storage are refused where their extents meet."""
+    if out is None or out.numel() == 0:
+        return
+
+    def extent(t):
+        last = sum((n - 1) * abs(st) for n, st in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+    a0, a1 = extent(out)
+    for name, t in inputs.items():
+        if t is None or t.numel() == 0:
+            continue
+        b0, b1 = extent(t)
+        if a0 < b1 and b0 < a1 and t.device == out.device:
+            raise ValueError(f"out: shares memory with {name}")
+
+
+@contextlib.contextmanager
+def _device_of(stream, **tensors):
+    """Every tensor of a call on one CUDA device (and the stream too), which
+    is made current for the call."""
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        where = ", ".join(f"{k} on {t.device}" for k, t in tensors.items() if t is not None)
+        raise ValueError(f"tensors must lie on one CUDA device: {where}")
+    dev = next(iter(devs))
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+    with torch.cuda.device(dev):
+        yield dev
+
+
+class PagedStore:
+    """A kvi8r cache in pages, held in torch tensors: int8 codes [pages,
+    kv_heads, page_size, 128] and fp16 scales [pages, kv_heads, page_size]
+    for K and for V.  Pool row r is slot r % page_size of page
+    r // page_size."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        _need(k_codes, "k_codes", torch.int8)
+        if k_codes.dim() != 4 or k_codes.shape[3] != HEAD_DIM:
+            raise ValueError(f"k_codes: shape {tuple(k_codes.shape)}, expected [pages, kv_heads, page_size, {HEAD_DIM}]")
+        self.k_codes, self.v_codes = k_codes, v_codes
+        self.k_scales, self.v_scales = k_scales, v_scales
+        self.pages, self.kv_heads, self.page_size = (int(x) for x in k_codes.shape[:3])
+        if self.page_size not in PAGE_SIZES:
+            raise ValueError(f"page_size {self.page_size}, expected one of {PAGE_SIZES}")
+        self.c_struct()
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int = 64, device="cuda") -> "PagedStore":
+        """Uninitialised pages: a row holds something once it is appended."""
+        kc, vc = (torch.empty((pages, kv_heads, page_size, HEAD_DIM), dtype=torch.int8, device=device)
+                  for _ in range(2))
+        ks, vs = (torch.empty((pages, kv_heads, page_size), dtype=torch.float16, device=device) for _ in range(2))
+        return cls(kc, vc, ks, vs)
+
+    def tensors(self) -> dict:
+        return {"store.k_codes": self.k_codes, "store.v_codes": self.v_codes, "store.k_scales": self.k_scales,
+                "store.v_scales": self.v_scales}
+
+    def c_struct(self) -> h3kv_paged_store:
+        shape = (self.pages, self.kv_heads, self.page_size)
+        _need(self.k_codes, "store.k_codes", torch.int8, (*shape, HEAD_DIM))
+        _need(self.v_codes, "store.v_codes", torch.int8, (*shape, HEAD_DIM))
+        _need(self.k_scales, "store.k_scales", torch.float16, shape)
+        _need(self.v_scales, "store.v_scales", torch.float16, shape)
+        return h3kv_paged_store(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scales), _ptr(self.v_scales),
+                                *shape, HEAD_DIM)
+
+    def nbytes(self) -> int:
+        return int(h3kv_paged_store_bytes(self.pages, self.kv_heads, self.page_size, HEAD_DIM))
+
+
+def paged_append(K: torch.Tensor, V: torch.Tensor, store: PagedStore, rows: torch.Tensor, stream=None) -> None:
+    """h3kv_paged_append: row i of bf16 K, V [kv_heads, n, 128] rotated,
+    quantised and written to pool row rows[i] (int32 [n]; negative: left
+    out).  No pool row may be named twice."""
+    k, v = _need_strided(K, "K", store.kv_heads), _need_strided(V, "V", store.kv_heads, int(K.shape[1]))
+    n = int(K.shape[1])
+    _need_index(rows, "rows", (n,))
+    st = store.c_struct()
+    with _device_of(stream, K=K, V=V, rows=rows, **store.tensors()):
+        check(h3kv_paged_append(ctypes.byref(k), ctypes.byref(v), _ptr(rows), n, ctypes.byref(st), _stream(stream)),
+              "h3kv_paged_append")
+
+
+def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = None, V: torch.Tensor | None = None,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """h3kv_paged_read: pool rows rows[i] (int32 [n]; negative: a row of
+    zeros) dequantised, un-rotated and rounded to bf16 [kv_heads, n, 128]."""
+    _need_index(rows, "rows")
+    if rows.dim() != 1:
+        raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [n]")
+    n = int(rows.shape[0])
+    st = store.c_struct()
+    with _device_of(stream, rows=rows, **store.tensors()) as dev, _on(stream):
+        K = torch.empty((store.kv_heads, n, HEAD_DIM), dtype=torch.bfloat16, device=dev) if K is None else K
+        V = torch.empty((store.kv_heads, n, HEAD_DIM), dtype=torch.bfloat16, device=dev) if V is None else V
+    k, v = _need_strided(K, "K", store.kv_heads, n), _need_strided(V, "V", store.kv_heads, n)
+    _need_apart(K, V=V if V.data_ptr() == K.data_ptr() else None, rows=rows)
+    with _device_of(stream, K=K, V=V, rows=rows, **store.tensors()):
+        check(h3kv_paged_read(ctypes.byref(st), _ptr(rows), n, ctypes.byref(k), ctypes.byref(v), _stream(stream)),
+              "h3kv_paged_read")
+    return K, V
+
+
+def paged_copy(store: PagedStore, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """h3kv_paged_copy: page src[i] copied to page dst[i] (int32 [n]; a pair
+    with a negative entry is left out).  No page may be a dst twice, or both a
+    dst and a src."""
+    _need_index(src, "src")
+    if src.dim() != 1:
+        raise ValueError(f"src: shape {tuple(src.shape)}, expected [n]")
+    _need_index(dst, "dst", src.shape)
+    st = store.c_struct()
+    with _device_of(stream, src=src, dst=dst, **store.tensors()):
+        check(h3kv_paged_copy(ctypes.byref(st), _ptr(src), _ptr(dst), int(src.shape[0]), _stream(stream)),
+              "h3kv_paged_copy")
+
+
+def _need_table(page_table, lengths, cu_nodes) -> int:
+    _need_index(cu_nodes, "cu_nodes")
+    if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
+        raise ValueError(f"cu_nodes: shape {tuple(cu_nodes.shape)}, expected [seqs + 1]")
+    seqs = int(cu_nodes.shape[0]) - 1
+    _need_index(lengths, "lengths", (seqs,))
+    _need_index(page_table, "page_table")
+    if page_table.dim() != 2 or page_table.shape[0] != seqs:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [{seqs}, max_pages]")
+    return seqs
+
+
+def paged_keep(store: PagedStore, page_table: torch.Tensor, lengths: torch.Tensor, cu_nodes: torch.Tensor,
+               keep: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h3kv_paged_keep: of each sequence's last cu_nodes[i+1] - cu_nodes[i]
+    cached rows (at most 64), those with keep (uint8 or bool [nodes]) set move
+    up behind the rows before them, in order -> the lengths that are left
+    (int32 [seqs]).  The pages of those rows belong to that sequence alone."""
+    seqs = _need_table(page_table, lengths, cu_nodes)
+    _need(keep, "keep", torch.bool if isinstance(keep, torch.Tensor) and keep.dtype == torch.bool else torch.uint8)
+    if keep.dim() != 1:
+        raise ValueError(f"keep: shape {tuple(keep.shape)}, expected [nodes]")
+    st = store.c_struct()
+    with _device_of(stream, page_table=page_table, lengths=lengths, cu_nodes=cu_nodes, keep=keep, out=out,
+                    **store.tensors()) as dev:
+        with _on(stream):
+            out = torch.empty((seqs,), dtype=torch.int32, device=dev) if out is None else out
+        _need_index(out, "out", (seqs,))
+        _need_apart(out, lengths=lengths, cu_nodes=cu_nodes, page_table=page_table, keep=keep)
+        check(h3kv_paged_keep(ctypes.byref(st), _ptr(page_table), int(page_table.shape[1]), _ptr(lengths),
+                              _ptr(cu_nodes), seqs, _ptr(keep), int(keep.shape[0]), _ptr(out), _stream(stream)),
+              "h3kv_paged_keep")
+    return out
+
+
+def _need_lse(lse, Q) -> None:
+    if lse is not None:
+        _need(lse, "lse", torch.float32, Q.shape[:2])
+
+
+def attend_tree(Q: torch.Tensor, store: PagedStore, page_table: torch.Tensor, lengths: torch.Tensor,
+                cu_nodes: torch.Tensor, parents: torch.Tensor | None = None, softmax_scale: float = 0.0,
+                out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h3kv_attend_tree: bf16 Q [q_heads, nodes, 128], the drafted nodes of
+    sequence i in rows cu_nodes[i] .. cu_nodes[i+1]-1 (at most 64), attends
+    over the sequence's lengths[i] cached rows, the last of which are the
+    nodes themselves -> bf16 like Q.  A node sees the rows before the drafted
+    ones and its own path to the root by ``parents`` (int32 [nodes]; None: a
+    plain run of tokens).  ``lse`` (fp32 [q_heads, nodes]) takes the
+    log-sum-exp of the scores.  ``workspace`` (uint8, >=
+    h3kv_attend_tree_workspace_bytes) is created here if not given."""
+    q = _need_strided(Q, "Q")
+    heads, nodes = int(Q.shape[0]), int(Q.shape[1])
+    if store.kv_heads < 1 or heads % store.kv_heads != 0:
+        raise ValueError(f"Q: {heads} heads, not a multiple of the store's {store.kv_heads}")
+    seqs = _need_table(page_table, lengths, cu_nodes)
+    if parents is not None:
+        _need_index(parents, "parents", (nodes,))
+    _need_lse(lse, Q)
+    st = store.c_struct()
+    with _device_of(stream, Q=Q, page_table=page_table, lengths=lengths, cu_nodes=cu_nodes, parents=parents, out=out,
+                    lse=lse, workspace=workspace, **store.tensors()) as dev:
+        need = int(h3kv_attend_tree_workspace_bytes(heads, store.kv_heads, nodes, seqs))
+        with _on(stream):
+            out = torch.empty((heads, nodes, HEAD_DIM), dtype=torch.bfloat16, device=dev) if out is None else out
+            if workspace is None:
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        o = _need_strided(out, "out", heads, nodes)
+        _need(workspace, "workspace", torch.uint8)
+        _need_apart(out, Q=Q, lse=lse, workspace=workspace)
+        check(h3kv_attend_tree(ctypes.byref(q), heads, nodes, ctypes.byref(st), _ptr(page_table),
+                               int(page_table.shape[1]), _ptr(lengths), _ptr(cu_nodes), seqs, _ptr(parents),
+                               float(softmax_scale), ctypes.byref(o), _ptr(lse), _ptr(workspace), workspace.numel(),
+                               _stream(stream)), "h3kv_attend_tree")
+    return out
+
+
+def attend_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor,
+                  cu_k: torch.Tensor | None = None, causal: bool = True, softmax_scale: float = 0.0,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h3kv_attend_prompt: bf16 Q [q_heads, q_rows, 128] over bf16 K, V
+    [kv_heads, k_rows, 128], sequences packed by cu_q and cu_k (int32
+    [seqs + 1]; cu_k None: cu_q), causal from the last row back or not ->
+    bf16 like Q.  ``lse`` (fp32 [q_heads, q_rows]) takes the log-sum-exp of
+    the scores.  Rows of no sequence are left as they are in ``out``."""
+    q, k = _need_strided(Q, "Q"), _need_strided(K, "K")
+    heads, kv_heads, rows = int(Q.shape[0]), int(K.shape[0]), int(Q.shape[1])
+    v = _need_strided(V, "V", kv_heads, int(K.shape[1]))
+    if kv_heads < 1 or heads % kv_heads != 0:
+        raise ValueError(f"Q: {heads} heads, not a multiple of K's {kv_heads}")
+    _need_index(cu_q, "cu_q")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError(f"cu_q: shape {tuple(cu_q.shape)}, expected [seqs + 1]")
+    cu_k = cu_q if cu_k is None else cu_k
+    _need_index(cu_k, "cu_k", cu_q.shape)
+    _need_lse(lse, Q)
+    with _device_of(stream, Q=Q, K=K, V=V, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse) as dev:
+        with _on(stream):
+            out = torch.empty((heads, rows, HEAD_DIM), dtype=torch.bfloat16, device=dev) if out is None else out
+        o = _need_strided(out, "out", heads, rows)
+        _need_apart(out, Q=Q, K=K, V=V, lse=lse)
+        check(h3kv_attend_prompt(ctypes.byref(q), heads, rows, ctypes.byref(k), ctypes.byref(v), kv_heads,
+                                 int(K.shape[1]), _ptr(cu_q), _ptr(cu_k), int(cu_q.shape[0]) - 1, int(bool(causal)),
+                                 float(softmax_scale), ctypes.byref(o), _ptr(lse), _stream(stream)),
+              "h3kv_attend_prompt")
+    return out
+
+
 def sync_status(stream=None) -> None:
-    """Synchronise the stream and raise if a kernel recorded a wait timeout."""
+    """Synchronise the stream and raise if a kernel recorded a wait timeout or
+    an index out of range."""
     check(h3kv_sync_status(_stream(stream)), "h3kv_sync_status")

@@ -10,6 +10,7 @@
 #include "kernels.h"
 #include "ptx.cuh"
 #include "launch_order.h"
+#include "serve.h"
 
 namespace {
 
@@ -215,6 +216,30 @@ float scale_log2_of(float softmax_scale) {
 
 }  // namespace
 
+namespace h3kv {
+
+h3kv_status serve_device(ServeDevice *out) {
+  DeviceInfo *d = nullptr;
+  const h3kv_status st = device_info(&d);
+  if (st != H3KV_OK) return st;
+  *out = {d->err, d->num_sms, g_timeout_ns.load(), g_withhold_p_tile1.load()};
+  return H3KV_OK;
+}
+
+bool encode_rows_bf16(CUtensorMap *m, const h3kv_rows &r, int64_t heads, int64_t rows, uint32_t box_rows) {
+  // the stride of an axis of one entry is never used; give it a valid value
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rows > 1 ? r.row_stride : H3KV_HEAD_DIM) * 2,
+                                 static_cast<cuuint64_t>(heads > 1 ? r.head_stride : H3KV_HEAD_DIM) * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.data, dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace h3kv
+
 extern "C" {
 
 uint32_t h3kv_abi_version(void) { return H3KV_ABI_VERSION; }
@@ -232,6 +257,7 @@ const char *h3kv_strerror(h3kv_status status) {
     case H3KV_ERR_UNSUPPORTED: return "unsupported (head_dim must be 128; device must be sm_103)";
     case H3KV_ERR_CUDA: return "CUDA runtime error";
     case H3KV_ERR_DEVICE_TIMEOUT: return "a bounded in-kernel wait ran out";
+    case H3KV_ERR_DEVICE_DATA: return "an index array in device memory held a value out of range";
   }
   return "unknown status";
 }
@@ -841,7 +867,9 @@ h3kv_status h3kv_sync_status(void *stream) {
     if (cudaDeviceSynchronize() != cudaSuccess) return H3KV_ERR_CUDA;
     // bit 0: a bounded wait ran out; bit 1: the shared-memory base could not
     // be aligned within the requested slack (the kernel returned at entry)
-    return (word & h3kv::kErrTimeout) ? H3KV_ERR_DEVICE_TIMEOUT : H3KV_ERR_CUDA;
+    // bit 2: a serving kernel met an index out of range
+    if (word & h3kv::kErrTimeout) return H3KV_ERR_DEVICE_TIMEOUT;
+    return (word & h3kv::kErrIndex) ? H3KV_ERR_DEVICE_DATA : H3KV_ERR_CUDA;
   }
   return H3KV_OK;
 }
