@@ -1,0 +1,383 @@
+// serve_attend.cuh -- the attention pipeline of the serving operators on sm_103a
+// tensor cores (tcgen05 + TMEM): packed prompts over bf16 K/V, and trees of
+// drafted tokens over the paged kvi8r cache.
+//
+// A CTA works through segments: up to 256 query rows that share one kv head,
+// over a run of 128-key tiles.  Two softmax warpgroups (thread = row = TMEM
+// lane) keep two score tiles in flight, so that one's softmax overlaps the
+// other's matrix products:
+//   rows > 128 ("two"):  warpgroup q owns rows 128 q .. 128 q + 127 and sees
+//                        every key tile;
+//   rows <= 128:         both own the same rows, warpgroup q sees the key tiles
+//                        of parity q, and the two running softmaxes are joined
+//                        by their log-sum-exp at the segment's end.
+// So a single token keeps both halves of the pipeline busy, and its keys are
+// read once.
+//
+// Warp roles (512 threads):
+//   warps 0-3, 4-7  softmax, correction and epilogue of stream 0 / 1
+//   warps 8-11      cache: in-place int8 -> fp16 dequantisation of K and V
+//                   tiles; prompts: zeroing of the V rows behind a sequence
+//   warp 12         producer: bulk / TMA copies into the K and V rings
+//   warp 13         TMEM allocation and tcgen05.mma issue
+// TMEM (512 columns, fp32): S0 [0,128), S1 [128,256), P over the first 64
+// columns of its S, O0 [256,384), O1 [384,512).
+#pragma once
+
+#include <math.h>
+
+#include "attend.cuh"
+#include "serve.h"
+
+namespace h3kv {
+namespace serve {
+
+using attn::kBM;
+using attn::kBN;
+using attn::kChunkBytes;
+using attn::kLazyRescaleLog2;
+using attn::kNK;
+using attn::kNV;
+using attn::kThreads;
+using attn::kTileBytes;
+using attn::warp_wait;
+
+// Register split per warpgroup, sums to 512 = 4 x 128 (the launch's share).
+constexpr uint32_t kRegSoftmax = 184, kRegDequant = 72, kRegIssue = 72;
+static_assert(2 * kRegSoftmax + kRegDequant + kRegIssue == 512, "register split");
+
+// Stands for "no key yet" in a running maximum: finite, so that no difference
+// of two infinities arises, and below any score of bf16 or fp16 operands that
+// has a weight at all.
+constexpr float kNoMax = -1e30f;
+
+struct Smem {
+  uint8_t q[2][kTileBytes];
+  uint8_t k[kNK][kTileBytes];
+  uint8_t v[kNV][kTileBytes];
+  float2 ml[kBM];  // stream 1's (max, sum) for the join with stream 0
+  uint64_t q_full[2];
+  uint64_t k_load[kNK], k_ready[kNK], k_free[kNK];
+  uint64_t v_load[kNV], v_ready[kNV], v_free[kNV];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full, drain;
+  uint64_t v_tail, v_fixed;  // prompts: a ragged last V tile copied; its rest zeroed
+  int64_t scan_prefix, scan_total;
+  int64_t warp_sum[16];
+  int scan_seq;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// Ring slot and phase, advanced tile by tile over all segments.
+template <int kDepth>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kDepth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// One segment: key tiles t0 .. t0 + n - 1 of a sequence for up to 256 rows.
+struct Seg {
+  int n;          // key tiles that any row sees
+  int n0;         // ... that stream 0's rows see (two: n0 <= n; else n)
+  int t0;
+  int two;
+  int rows;
+  int row0;       // first row in the sequence's row numbering
+  int head;       // prompt: query head; cache: kv head
+  int64_t keys;   // keys of the sequence
+  int64_t q_base; // first row of the sequence in Q
+  int64_t k_base; // prompt: first row of the sequence in K; cache: its first page table entry
+  int64_t diff;   // prompt, causal: row t sees the keys u <= t + diff
+  int nodes;      // cache: drafted nodes
+  int seq;
+  int whole;      // every key tile of the rows is in this segment
+};
+
+// Tiles of stream q in a segment: first, step and end.
+__device__ __forceinline__ int first_tile(const Seg &s, int q) { return s.two ? 0 : q; }
+__device__ __forceinline__ int tile_step(const Seg &s) { return s.two ? 1 : 2; }
+__device__ __forceinline__ int end_tile(const Seg &s, int q) { return s.two && q == 0 ? s.n0 : s.n; }
+__device__ __forceinline__ bool has_tiles(const Seg &s, int q) { return first_tile(s, q) < end_tile(s, q); }
+
+__device__ __forceinline__ void init_barriers(Smem &sm, bool cache) {
+  for (int q = 0; q < 2; ++q) {
+    mbar_init(smem_u32(&sm.q_full[q]), cache ? 4 : 1);
+    mbar_init(smem_u32(&sm.s_full[q]), 1);
+    mbar_init(smem_u32(&sm.p_full[q]), 4);
+  }
+  for (int s = 0; s < kNK; ++s) {
+    mbar_init(smem_u32(&sm.k_load[s]), 1);
+    mbar_init(smem_u32(&sm.k_ready[s]), 4);
+    mbar_init(smem_u32(&sm.k_free[s]), 1);
+  }
+  for (int s = 0; s < kNV; ++s) {
+    mbar_init(smem_u32(&sm.v_load[s]), 1);
+    mbar_init(smem_u32(&sm.v_ready[s]), 4);
+    mbar_init(smem_u32(&sm.v_free[s]), 1);
+  }
+  mbar_init(smem_u32(&sm.o_full), 1);
+  mbar_init(smem_u32(&sm.drain), 1);
+  mbar_init(smem_u32(&sm.v_tail), 1);
+  mbar_init(smem_u32(&sm.v_fixed), 4);
+  sm.abort = 0;
+  fence_mbar_init();
+}
+
+// Sum of `v` over the block; every thread gets it.  All threads call it.
+__device__ __forceinline__ int64_t block_sum(Smem &sm, int64_t v) {
+  const int warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm.warp_sum[warp] = v;
+  __syncthreads();
+  int64_t t = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) t += sm.warp_sum[w];
+  return t;
+}
+
+// Sum of the values of the threads before this one, and of all.
+__device__ __forceinline__ int64_t block_prefix(Smem &sm, int64_t v, int64_t *total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t inc = v;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
+    if (lane >= x) inc += o;
+  }
+  __syncthreads();
+  if (lane == 31) sm.warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int64_t t = sm.warp_sum[w];
+    before += w < warp ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+// ------------------------------------------------------------- MMA issuer --
+// The warp runs this converged; one elected lane issues.  Order per key tile
+// and stream: PV of the tile, then QK of the stream's next tile, so that the
+// completion of a QK also covers the PV before it.
+struct MmaState {
+  uint32_t go, tmem, dhi, lq0, lk0, lv0, idesc_qk, idesc_pv;
+  Ring<kNK> k;        // the next key tile whose QK is to be issued first
+  Ring<kNV> v;
+  uint32_t p_phase[2] = {0, 0};
+  uint32_t q_phase[2] = {0, 0};
+};
+
+__device__ __forceinline__ void mma_setup(MmaState &m, Smem &sm, bool bf16) {
+  m.go = elect_one();
+  m.tmem = sm.tmem_base;
+  m.idesc_qk = idesc_f16(bf16, false, kBM, kBN);
+  m.idesc_pv = idesc_f16(bf16, true, kBM, 128);
+  const uint64_t dq0 = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024);
+  m.dhi = static_cast<uint32_t>(dq0 >> 32);
+  m.lq0 = static_cast<uint32_t>(dq0);
+  m.lk0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sm.k[0]), 16, 1024));
+  m.lv0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sm.v[0]), kChunkBytes, 1024));
+}
+
+__device__ __forceinline__ void issue_qk(const MmaState &m, int q, int ks) {
+  const uint32_t lq = m.lq0 + q * (kTileBytes >> 4), lk = m.lk0 + ks * (kTileBytes >> 4);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
+    mma_ss(m.go, m.tmem + q * 128, lq + off, lk + off, m.dhi, m.idesc_qk, kk > 0);
+  }
+}
+
+__device__ __forceinline__ void issue_pv(const MmaState &m, int q, int vs, bool acc) {
+  const uint32_t lv = m.lv0 + vs * (kTileBytes >> 4);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(m.go, m.tmem + 256 + q * 128, m.tmem + q * 128 + kk * 8, lv + (kk * 2048 >> 4), m.dhi, m.idesc_pv,
+           (acc || kk > 0) ? 1u : 0u);
+}
+
+// One segment's products.  kReady: tiles are handed over by the dequantising
+// warps (k_ready, v_ready); otherwise by the copies (k_load, v_load), and a
+// ragged last V tile by v_fixed.
+template <bool kReady>
+__device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s, bool ragged, const WaitCtx &w) {
+  uint64_t *k_rdy = kReady ? sm.k_ready : sm.k_load;
+  uint64_t *v_rdy = kReady ? sm.v_ready : sm.v_load;
+  // the stream's QK of tile t: waits for the tile (its first user does), and
+  // releases it after its last user
+  auto qk = [&](int q, bool first_user, bool last_user) {
+    if (first_user) {
+      if (!warp_wait(smem_u32(&k_rdy[m.k.slot]), m.k.phase, w)) return false;
+      tc_fence_after();
+    }
+    issue_qk(m, q, m.k.slot);
+    mma_commit(m.go, smem_u32(&sm.s_full[q]));
+    if (last_user) {
+      mma_commit(m.go, smem_u32(&sm.k_free[m.k.slot]));
+      m.k.next();
+    }
+    return true;
+  };
+  for (int q = 0; q < 2; ++q) {
+    if (!has_tiles(s, q)) continue;
+    if (!warp_wait(smem_u32(&sm.q_full[q]), m.q_phase[q], w)) return false;
+    m.q_phase[q] ^= 1u;
+    tc_fence_after();
+    // two: both streams start on tile 0 (stream 1 alone where stream 0 has none)
+    const bool first_user = !s.two || q == 0 || s.n0 == 0;
+    if (!qk(q, first_user, !s.two || q == 1)) return false;
+  }
+  const int step = tile_step(s);
+  for (int t = 0; t < s.n; ++t) {
+    const bool fixed = !kReady && ragged && t == s.n - 1;
+    if (!warp_wait(fixed ? smem_u32(&sm.v_fixed) : smem_u32(&v_rdy[m.v.slot]), fixed ? 0u : m.v.phase, w))
+      return false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = s.two ? i : (t & 1);
+      if (!s.two && i == 1) break;
+      if (t >= end_tile(s, q)) continue;
+      if (!warp_wait(smem_u32(&sm.p_full[q]), m.p_phase[q], w)) return false;
+      m.p_phase[q] ^= 1u;
+      tc_fence_after();
+      issue_pv(m, q, m.v.slot, t != first_tile(s, q));
+      if (!s.two || q == 1) mma_commit(m.go, smem_u32(&sm.v_free[m.v.slot]));
+      const int tn = t + step;
+      if (tn < end_tile(s, q)) {
+        const bool first_user = !s.two || q == 0 || tn >= s.n0;
+        if (!qk(q, first_user, !s.two || q == 1)) return false;
+      }
+    }
+    m.v.next();
+  }
+  mma_commit(m.go, smem_u32(&sm.o_full));
+  return true;
+}
+
+// ---------------------------------------------------------------- softmax --
+struct Row {
+  float m, l;  // running maximum (raw score units) and sum of this thread's row
+};
+
+// One 128-key tile: S from TMEM, mask, running maximum, P back to TMEM.
+// `masked` (warp-uniform): only the columns set in `see` count.
+template <bool kF16>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, bool masked,
+                                             const uint32_t (&see)[4], float c2, Row &r) {
+  float s[128];
+  float m4[4];
+  tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
+  float mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < 128; ++c) s[c] = (see[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
+    float m8[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m8[u] = fmax3(s[u], s[u + 8], s[u + 16]);
+#pragma unroll
+    for (int c = 24; c < 120; c += 16) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) m8[u] = fmax3(m8[u], s[c + u], s[c + 8 + u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], s[120 + u]);
+    mt = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+    mt = fmaxf(mt, kNoMax);
+  }
+  if (first) {
+    r.m = mt;
+    r.l = 0.f;
+  } else {
+    // O is rescaled only when the maximum grows by more than 2^8 (exact: the
+    // weights are relative to r.m, whatever it is)
+    const bool need = (mt - r.m) * c2 > kLazyRescaleLog2;
+    if (__any_sync(0xffffffffu, need)) {
+      const float alpha = need ? ex2((r.m - mt) * c2) : 1.f;
+      if (need) {
+        r.l *= alpha;
+        r.m = mt;
+      }
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+        tmem_st16(tO + c * 16, o);
+      }
+    }
+  }
+  const float2 cc = make_float2(c2, c2), nm = make_float2(-r.m * c2, -r.m * c2);
+  float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const int c = h * 64 + 2 * k;
+      float2 e = __ffma2_rn(make_float2(s[c], s[c + 1]), cc, nm);
+      e.x = ex2(e.x);
+      e.y = ex2(e.y);
+      if (k & 1) acc1 = __fadd2_rn(acc1, e);
+      else acc0 = __fadd2_rn(acc0, e);
+      pk[k] = attn::pack2<kF16>(e.x, e.y);
+    }
+    tmem_st32(tS + h * 32, pk);
+  }
+  tmem_wait_st();
+  const float2 acc = __fadd2_rn(acc0, acc1);
+  r.l += acc.x + acc.y;
+}
+
+// Columns below `n` of a 128-column tile, as bits.
+__device__ __forceinline__ void prefix_mask(int64_t n, uint32_t (&see)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int64_t k = n - 32 * g;
+    see[g] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+  }
+}
+
+// The rows' O from TMEM times `ga`, plus stream 1's times `gb` when joined.
+__device__ __forceinline__ void load_o(uint32_t tO0, uint32_t tO1, bool joined, float ga, float gb, float (&o)[128]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float x[32];
+    tmem_ld32(tO0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[32 * c + k] = x[k] * ga;
+    if (joined) {
+      tmem_ld32(tO1 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[32 * c + k] = fmaf(x[k], gb, o[32 * c + k]);
+    }
+  }
+}
+
+// Joins stream 1's (max, sum) into r: the weights of the two streams' O.
+__device__ __forceinline__ void join_rows(Row &r, float2 other, float c2, float &ga, float &gb) {
+  const float m = fmaxf(r.m, other.x);
+  ga = ex2((r.m - m) * c2);
+  gb = ex2((other.x - m) * c2);
+  r.l = fmaf(r.l, ga, other.y * gb);
+  r.m = m;
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+}  // namespace serve
+}  // namespace h3kv

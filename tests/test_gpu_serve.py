@@ -77,6 +77,19 @@ def test_prompt_lengths(cuda, n, causal):
     prompt_case([n], [n], 2, 1, causal, seed=n)
 
 
+@pytest.mark.parametrize("n", [128, 129, 255, 256, 257, 385, 513, 640])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_lengths_with_many_heads(cuda, n, causal):
+    # enough heads that a CTA owns 256 rows (two row tiles over the same keys)
+    prompt_case([n], [n], 160, 4, causal, seed=n)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_packed_with_many_heads(cuda, causal):
+    qn, pre = [140, 300, 256, 1, 129], [500, -200, 77, 0, 128]
+    prompt_case(qn, [q + p for q, p in zip(qn, pre)], 64, 2, causal, seed=21, layout="token", pad=9)
+
+
 @pytest.mark.parametrize("hq,hk", [(1, 1), (8, 8), (8, 2), (6, 2), (32, 1), (24, 8)])
 def test_prompt_head_groups(cuda, hq, hk):
     prompt_case([70, 1, 300], [70, 1, 300], hq, hk, seed=5)
@@ -117,6 +130,7 @@ def test_prompt_many_short_sequences(cuda):
 
 def test_prompt_long(cuda):
     prompt_case([1900], [4100], 3, 1, seed=10)
+    prompt_case([1500], [1500], 52, 52, seed=11)
 
 
 def test_prompt_values_of_other_sequences_do_not_reach(cuda):
