@@ -1,26 +1,434 @@
-// attend_tree.cu -- attention of drafted tokens over the paged kvi8r cache.
-#include <math.h>
-
-#include "ptx.cuh"
-#include "serve.h"
+// attend_tree.cu -- attention of drafted tokens over the paged kvi8r cache (the
+// pipeline of serve_attend.cuh), keys split evenly over the SMs.
+//
+// The work is the list of all (sequence, kv head, 256-row tile, 128-key tile)
+// units in that order.  One CTA per SM takes an equal run of it, whatever the
+// lengths: a segment is the part of a run that belongs to one (sequence, head,
+// row tile).  A segment that holds every key tile of its rows writes the
+// output; the others write their un-normalised output with (max, sum) to the
+// workspace, and a second kernel joins each row's parts in order.  A CTA has at
+// most two such parts: the end of an item begun before its run, and the
+// beginning of one that goes on behind it.
+#include "serve_attend.cuh"
 
 namespace h3kv {
+namespace serve {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kMaxCtas = 152;
+constexpr int kItemRows = 2 * kBM;
 
-// One warp for a query row of one head, as a loop over the row's keys.
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < a.seqs; i += blockDim.x) {
-      const int64_t c0 = __ldg(a.cu_nodes + i), c1 = __ldg(a.cu_nodes + i + 1), len = __ldg(a.lengths + i);
-      if (c0 < 0 || c1 < c0 || c1 > a.nodes || c1 - c0 > H3KV_TREE_MAX_NODES || len < c1 - c0 ||
-          len > (a.max_pages << a.p.page_shift))
-        atomicOr(a.p.err, kErrIndex);
+// Workspace: prefix of units before each sequence (int64 [seqs + 1]), then
+// per CTA and part (max, sum) [rows] and un-normalised O [rows][128].
+struct Workspace {
+  int64_t *prefix;
+  float2 *ml;
+  float *o;
+  int rows;  // rows of a part
+};
+__host__ __device__ inline int part_rows(int group, int64_t nodes) {
+  const int64_t n = group * (nodes < H3KV_TREE_MAX_NODES ? nodes : H3KV_TREE_MAX_NODES);
+  return n < kItemRows ? static_cast<int>(n) : kItemRows;
+}
+__host__ __device__ inline size_t prefix_bytes(int32_t seqs) {
+  return (static_cast<size_t>(seqs + 1) * 8 + 255) / 256 * 256;
+}
+__device__ inline Workspace workspace_of(const TreeArgs &a) {
+  Workspace ws;
+  uint8_t *p = reinterpret_cast<uint8_t *>(a.workspace);
+  ws.rows = part_rows(a.group, a.nodes);
+  ws.prefix = reinterpret_cast<int64_t *>(p);
+  ws.o = reinterpret_cast<float *>(p + prefix_bytes(a.seqs));
+  ws.ml = reinterpret_cast<float2 *>(ws.o + static_cast<int64_t>(a.ctas) * 2 * ws.rows * 128);
+  return ws;
+}
+
+// A sequence's counts; tiles == 0: nothing to do (empty, or out of range).
+struct Counts {
+  int64_t q_base;
+  int32_t len, nodes, tiles, row_tiles;
+  int64_t units;
+  bool bad;
+};
+__device__ __forceinline__ Counts counts_of(const TreeArgs &a, int i) {
+  const int64_t c0 = __ldg(a.cu_nodes + i), c1 = __ldg(a.cu_nodes + i + 1), len = __ldg(a.lengths + i), m = c1 - c0;
+  Counts c;
+  c.bad = c0 < 0 || m < 0 || c1 > a.nodes || m > H3KV_TREE_MAX_NODES || len < m ||
+          len > (a.max_pages << a.p.page_shift) || len > INT32_MAX - 256;
+  const bool on = !c.bad && m > 0;
+  c.q_base = c0;
+  c.len = on ? static_cast<int32_t>(len) : 0;
+  c.nodes = on ? static_cast<int32_t>(m) : 0;
+  c.tiles = (c.len + kBN - 1) / kBN;
+  c.row_tiles = (c.nodes * a.group + kItemRows - 1) / kItemRows;
+  c.units = static_cast<int64_t>(c.tiles) * c.row_tiles * a.p.kv_heads;
+  return c;
+}
+
+// CTAs that get work, each at least one unit, and the first unit of one.
+__device__ __forceinline__ int working(const TreeArgs &a, int64_t total) {
+  return total < a.ctas ? static_cast<int>(total) : a.ctas;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+
+// The segments of a run of units, one after the other.  Every role walks its
+// own copy.
+struct Walk {
+  int64_t u, end;     // units left: [u, end)
+  int64_t before;     // units before sequence `seq`
+  int seq;
+  Counts c;
+  __device__ __forceinline__ void start(const TreeArgs &a, const Smem &sm, int64_t u0, int64_t u1) {
+    u = u0;
+    end = u1;
+    seq = sm.scan_seq;
+    before = sm.scan_prefix;
+    if (u < end) c = counts_of(a, seq);
+  }
+  __device__ __forceinline__ bool next(const TreeArgs &a, Seg *s) {
+    if (u >= end) return false;
+    while (u >= before + c.units) {
+      before += c.units;
+      c = counts_of(a, ++seq);
+    }
+    const int64_t w = u - before, item = w / c.tiles;
+    s->t0 = static_cast<int>(w - item * c.tiles);
+    const int64_t left = end - u;
+    s->n = c.tiles - s->t0 < left ? c.tiles - s->t0 : static_cast<int>(left);
+    s->n0 = s->n;
+    s->head = static_cast<int>(item / c.row_tiles);
+    s->row0 = static_cast<int>(item - static_cast<int64_t>(s->head) * c.row_tiles) * kItemRows;
+    const int rows = c.nodes * a.group - s->row0;
+    s->rows = rows < kItemRows ? rows : kItemRows;
+    s->two = s->rows > kBM;
+    s->keys = c.len;
+    s->q_base = c.q_base;
+    s->k_base = static_cast<int64_t>(seq) * a.max_pages;
+    s->nodes = c.nodes;
+    s->seq = seq;
+    s->diff = 0;
+    s->whole = s->n == c.tiles;
+    u += s->n;
+    return true;
+  }
+};
+
+// Node j's path to its root as bits.
+__device__ __forceinline__ uint64_t path_of(const TreeArgs &a, int64_t q_base, int j) {
+  if (!a.parents) return (2ull << j) - 1;
+  uint64_t path = 0;
+  for (int n = j; n >= 0;) {
+    path |= 1ull << n;
+    const int up = __ldg(a.parents + q_base + n);
+    n = up >= 0 && up < n ? up : -1;
+  }
+  return path;
+}
+
+// The 128-column mask of a row for the tile at key `pos`: all keys below
+// `base`, and node i's key base + i where bit i of `path` is set.
+__device__ __forceinline__ void tree_mask(int32_t pos, int32_t base, uint64_t path, uint32_t (&see)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int32_t off = base - (pos + 32 * g);  // columns below off come before the nodes
+    if (off >= 32) see[g] = 0xffffffffu;
+    else if (off >= 0) see[g] = ((1u << off) - 1u) | static_cast<uint32_t>(path << off);
+    else see[g] = off > -64 ? static_cast<uint32_t>(path >> -off) : 0u;
+  }
+}
+
+// The page of the row at token `pos`; a page out of range is reported and
+// page 0 read in its place.
+__device__ __forceinline__ int32_t page_at(const TreeArgs &a, int64_t table, int32_t pos) {
+  const int32_t page = __ldg(a.page_table + table + (pos >> a.p.page_shift));
+  if (page < 0 || page >= a.p.pages) {
+    atomicOr(a.p.err, kErrIndex);
+    return 0;
+  }
+  return page;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Workspace ws = workspace_of(a);
+
+  // units of all sequences, then the sequence that holds this CTA's first one
+  int64_t mine = 0;
+  for (int i = tid; i < a.seqs; i += kThreads) {
+    const Counts c = counts_of(a, i);
+    mine += c.units;
+    if (c.bad && blockIdx.x == 0) atomicOr(a.p.err, kErrIndex);
+  }
+  const int64_t total = block_sum(sm, mine);
+  const int ctas = working(a, total), cta = static_cast<int>(blockIdx.x);
+  const int64_t u0 = cta < ctas ? first_unit(total, cta, ctas) : total;
+  const int64_t u1 = cta < ctas ? first_unit(total, cta + 1, ctas) : total;
+  int64_t before = 0;
+  for (int base = 0; base < a.seqs; base += kThreads) {
+    const int i = base + tid;
+    const int64_t n = i < a.seqs ? counts_of(a, i).units : 0;
+    int64_t all;
+    const int64_t at = before + block_prefix(sm, n, &all);
+    if (i < a.seqs && u0 >= at && u0 < at + n) {
+      sm.scan_seq = i;
+      sm.scan_prefix = at;
+    }
+    if (blockIdx.x == 0 && i < a.seqs) ws.prefix[i] = at;
+    before += all;
+    if (cta != 0 && u0 < before) break;
+  }
+  if (blockIdx.x == 0 && tid == 0) ws.prefix[a.seqs] = total;
+  if (u0 >= u1) return;
+
+  if (tid == 0) init_barriers(sm, true);
+  if (warp == 13) {
+    tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const WaitCtx w{a.p.err, &sm.abort, a.timeout_ns};
+  Walk walk;
+  Seg s;
+
+  if (warp < 8) {
+    // =================================================== softmax warpgroups
+    reg_alloc<kRegSoftmax>();
+    walk.start(a, sm, u0, u1);
+    const int q = warp >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + q * 128, tO = tmem + lane_base + 256 + q * 128;
+    const float c2 = a.scale_log2;
+    const int i = tid & 127;
+    uint32_t s_phase = 0, o_phase = 0;
+    while (walk.next(a, &s)) {
+      const int base_row = s.two ? q * kBM : 0;
+      const int r = base_row + i;
+      const int w0 = base_row + (warp & 3) * 32;  // the warp's first row
+      const bool warp_on = w0 < s.rows;
+      // q' = fp16(q H): the warp's rows one at a time, rotated across the warp,
+      // into the swizzled K-major tile.  The tile is free: this stream's last
+      // QK of the segment before has completed.
+      if (has_tiles(s, q)) {
+        const int n = s.rows - w0 < 32 ? s.rows - w0 : 32;
+        for (int rr = 0; rr < n; ++rr) {
+          const int x = s.row0 + w0 + rr, node = x / a.group;
+          const int h = s.head * a.group + (x - node * a.group);
+          const uint2 raw = *(reinterpret_cast<const uint2 *>(a.q.data + h * a.q.head_stride +
+                                                              (s.q_base + node) * a.q.row_stride) +
+                              lane);
+          float v[4] = {bf16lo_to_f32(raw.x), bf16hi_to_f32(raw.x), bf16lo_to_f32(raw.y), bf16hi_to_f32(raw.y)};
+          fwht128_warp(v, lane);
+          *reinterpret_cast<uint2 *>(sm.q[q] + (lane >> 4) * kChunkBytes +
+                                     sw128_off((warp & 3) * 32 + rr, (lane & 15) >> 1) + (lane & 1) * 8) =
+              make_uint2(pack_f16x2(v[0] * kInvSqrt128, v[1] * kInvSqrt128),
+                         pack_f16x2(v[2] * kInvSqrt128, v[3] * kInvSqrt128));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[q]));
+      }
+      const int32_t len = static_cast<int32_t>(s.keys), base_key = len - s.nodes;
+      uint64_t path = 0;
+      if (r < s.rows) path = path_of(a, s.q_base, (s.row0 + r) / a.group);
+      Row row{kNoMax, 0.f};
+      bool ok = true;
+      const int step = tile_step(s), end = end_tile(s, q), t_first = first_tile(s, q);
+      for (int t = t_first; t < end; t += step) {
+        if (!warp_wait(smem_u32(&sm.s_full[q]), s_phase, w)) {
+          ok = false;
+          break;
+        }
+        s_phase ^= 1u;
+        tc_fence_after();
+        if (warp_on) {
+          const int32_t pos = (s.t0 + t) * kBN;
+          const bool masked = pos + kBN > base_key;
+          uint32_t see[4];
+          tree_mask(pos, base_key, path, see);
+          softmax_tile<true>(tS, tO, t == t_first, masked, see, c2, row);
+        }
+        tc_fence_before();
+        __syncwarp();
+        // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
+        if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.p_full[q]));
+      }
+      ok = ok && warp_wait(smem_u32(&sm.o_full), o_phase, w);
+      o_phase ^= 1u;
+      tc_fence_after();
+      if (!s.two && q == 1) sm.ml[i] = make_float2(row.m, row.l);
+      ok = named_bar_and(1, 256, ok);
+      if (!ok) break;
+      if ((s.two || q == 0) && warp_on) {
+        const bool joined = !s.two && s.n > 1;
+        float ga = 1.f, gb = 0.f;
+        if (joined) join_rows(row, sm.ml[i], c2, ga, gb);
+        float o[128];
+        if (s.whole) {
+          const float inv = kInvSqrt128 / row.l;
+          load_o(tO, tO + 128, joined, ga * inv, gb * inv, o);
+          fwht128_packed(o);
+          if (r < s.rows) {
+            const int x = s.row0 + r, node = x / a.group, h = s.head * a.group + (x - node * a.group);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.o.data + h * a.o.head_stride +
+                                                   (s.q_base + node) * a.o.row_stride);
+#pragma unroll
+            for (int g = 0; g < 16; ++g)
+              dst[g] = make_uint4(pack_bf16x2(o[8 * g], o[8 * g + 1]), pack_bf16x2(o[8 * g + 2], o[8 * g + 3]),
+                                  pack_bf16x2(o[8 * g + 4], o[8 * g + 5]), pack_bf16x2(o[8 * g + 6], o[8 * g + 7]));
+            if (a.lse) a.lse[h * a.nodes + s.q_base + node] = kLn2 * (row.m * c2 + log2f(row.l));
+          }
+        } else {
+          load_o(tO, tO + 128, joined, ga, gb, o);
+          if (r < s.rows) {
+            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (s.t0 > 0 ? 0 : 1)) * ws.rows + r;
+            float4 *dst = reinterpret_cast<float4 *>(ws.o + at * 128);
+#pragma unroll
+            for (int g = 0; g < 32; ++g) dst[g] = make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+            ws.ml[at] = make_float2(row.m, row.l);
+          }
+        }
+      }
+      // stream 1's O and (max, sum) have been read
+      if (!s.two) named_bar_sync(2, 256);
+      tc_fence_before();
+    }
+  } else if (warp < 12) {
+    // ======================================================= dequantisers
+    reg_dealloc<kRegDequant>();
+    walk.start(a, sm, u0, u1);
+    const int dw = warp - 8;
+    const attn::DqOffsets off = attn::dq_offsets(dw, lane);
+    const int rr = 2 * (lane >> 4) + ((lane >> 2) & 1);
+    Ring<kNK> kr;
+    Ring<kNV> vr;
+    // The tile's 128 scales lie in the buffer's first half, each warp's 32 in
+    // the 64 bytes at its own first row: read by the whole warp before any of
+    // its lanes writes there.  Rows behind the sequence get scale 0.
+    auto dequant = [&](uint8_t *tile, int valid) {
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(tile + dw * 32 * 128) + rr;
+      uint16_t sc[8];
+#pragma unroll
+      for (int it = 0; it < 8; ++it) sc[it] = dw * 32 + rr + 4 * it < valid ? p[4 * it] : 0;
+      __syncwarp();
+      attn::dequant_tile(tile, sc, off);
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    bool ok = true;
+    while (ok && walk.next(a, &s)) {
+      for (int t = 0; t < s.n; ++t) {
+        const int64_t left = s.keys - static_cast<int64_t>(s.t0 + t) * kBN;
+        const int valid = left < kBN ? static_cast<int>(left) : kBN;
+        if (!(ok = warp_wait(smem_u32(&sm.k_load[kr.slot]), kr.phase, w))) break;
+        dequant(sm.k[kr.slot], valid);
+        if (lane == 0) mbar_arrive(smem_u32(&sm.k_ready[kr.slot]));
+        kr.next();
+        if (!(ok = warp_wait(smem_u32(&sm.v_load[vr.slot]), vr.phase, w))) break;
+        dequant(sm.v[vr.slot], valid);
+        if (lane == 0) mbar_arrive(smem_u32(&sm.v_ready[vr.slot]));
+        vr.next();
+      }
+    }
+  } else {
+    reg_dealloc<kRegIssue>();
+    walk.start(a, sm, u0, u1);
+    if (warp == 12) {
+      // ========================================================== producer
+      // A tile's codes come page by page (lanes 0-7) into the buffer's second
+      // half, its scales in pieces of at most 32 (lanes 8-15) into the first.
+      const int ps = a.p.page_size, sp = ps < 32 ? ps : 32;
+      const bool codes = lane < 8;
+      const int piece = lane & 7;
+      const int at = piece * (codes ? ps : sp);  // the piece's first row in the tile
+      int k_issued[kNK] = {0, 0, 0}, v_issued[kNV] = {0, 0};
+      Ring<kNK> kr;
+      Ring<kNV> vr;
+      bool ok = true;
+      while (ok && walk.next(a, &s)) {
+        for (int t = 0; t < s.n; ++t) {
+          const int32_t pos = (s.t0 + t) * kBN;
+          const int64_t left = s.keys - pos;
+          const int valid = left < kBN ? static_cast<int>(left) : kBN;
+          const bool on = lane < 16 && at < valid;
+          int64_t src = 0;
+          uint32_t bytes = 0, dst = 0;
+          if (on) {
+            const int32_t page = page_at(a, s.k_base, pos + at);
+            src = ((static_cast<int64_t>(page) * a.p.kv_heads + s.head) << a.p.page_shift) +
+                  ((pos + at) & (ps - 1));
+            if (codes) {
+              const int n = valid - at < ps ? valid - at : ps;
+              bytes = n * 128;
+              dst = kChunkBytes + at * 128;
+            } else {
+              bytes = sp * 2;
+              dst = (at >> 5) * 32 * 128 + (at & 31) * 2;
+            }
+          }
+          uint32_t sum = bytes;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          if (!(ok = warp_wait(smem_u32(&sm.k_free[kr.slot]), kr.phase ^ 1u, w))) break;
+          uint32_t bar = smem_u32(&sm.k_load[kr.slot]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+          __syncwarp();
+          if (on)
+            bulk_g2s(smem_u32(sm.k[kr.slot]) + dst,
+                     codes ? static_cast<const void *>(a.p.k_codes + src * 128)
+                           : static_cast<const void *>(a.p.k_scales + src),
+                     bytes, bar);
+          ++k_issued[kr.slot];
+          kr.next();
+          if (!(ok = warp_wait(smem_u32(&sm.v_free[vr.slot]), vr.phase ^ 1u, w))) break;
+          bar = smem_u32(&sm.v_load[vr.slot]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+          __syncwarp();
+          if (on)
+            bulk_g2s(smem_u32(sm.v[vr.slot]) + dst,
+                     codes ? static_cast<const void *>(a.p.v_codes + src * 128)
+                           : static_cast<const void *>(a.p.v_scales + src),
+                     bytes, bar);
+          ++v_issued[vr.slot];
+          vr.next();
+        }
+      }
+      if (sm.abort) {
+        // every copy that was issued must land before the CTA exits
+        for (int x = 0; x < kNK; ++x)
+          if (k_issued[x]) mbar_wait_drain(smem_u32(&sm.k_load[x]), (k_issued[x] - 1) & 1, kDrainNs);
+        for (int x = 0; x < kNV; ++x)
+          if (v_issued[x]) mbar_wait_drain(smem_u32(&sm.v_load[x]), (v_issued[x] - 1) & 1, kDrainNs);
+      }
+    } else if (warp == 13) {
+      MmaState m;
+      mma_setup(m, sm, false);
+      while (walk.next(a, &s))
+        if (!mma_segment<true>(m, sm, s, false, w)) break;
+      // every MMA issued must finish before TMEM is released
+      mma_commit(m.go, smem_u32(&sm.drain));
+      mbar_wait_drain(smem_u32(&sm.drain), 0, kDrainNs);
     }
   }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// One warp for an output row (a node of a query head): joins the parts of its
+// item over the CTAs that worked on it, in order, un-rotates and writes.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int64_t row = unit / a.q_heads;
   const int h = static_cast<int>(unit - row * a.q_heads);
   if (row >= a.nodes) return;
@@ -31,69 +439,64 @@ __global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeArgs a) {
     else hi = mid;
   }
   if (lo == a.seqs) return;
-  const int64_t c0 = __ldg(a.cu_nodes + lo), c1 = __ldg(a.cu_nodes + lo + 1);
-  const int64_t len = __ldg(a.lengths + lo), m_nodes = c1 - c0;
-  if (row < c0 || row >= c1) return;
-  if (c0 < 0 || c1 > a.nodes || m_nodes > H3KV_TREE_MAX_NODES || len < m_nodes ||
-      len > (a.max_pages << a.p.page_shift))
-    return;
-  const int j = static_cast<int>(row - c0);
-  uint64_t path = 0;
-  for (int n = j; n >= 0;) {
-    path |= 1ull << n;
-    const int up = a.parents ? __ldg(a.parents + c0 + n) : n - 1;
-    n = up >= 0 && up < n ? up : -1;
-  }
-  const uint2 qw = *reinterpret_cast<const uint2 *>(a.q.data + h * a.q.head_stride + row * a.q.row_stride + 4 * lane);
-  float q[4] = {bf16lo_to_f32(qw.x), bf16hi_to_f32(qw.x), bf16lo_to_f32(qw.y), bf16hi_to_f32(qw.y)};
-  fwht128_warp(q, lane);
-#pragma unroll
-  for (int t = 0; t < 4; ++t) q[t] = __half2float(__float2half_rn(q[t] * kInvSqrt128));
-  const int hk = h / a.group;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t u = 0; u < len; ++u) {
-    const int64_t node = u - (len - m_nodes);
-    if (node >= 0 && !((path >> node) & 1)) continue;
-    const int32_t page = __ldg(a.page_table + lo * a.max_pages + (u >> a.p.page_shift));
-    if (page < 0 || page >= a.p.pages) {
-      if (lane == 0) atomicOr(a.p.err, kErrIndex);
-      return;
-    }
-    const int64_t at = ((static_cast<int64_t>(page) * a.p.kv_heads + hk) << a.p.page_shift) +
-                       (u & (a.p.page_size - 1));
-    const uint32_t kw = reinterpret_cast<const uint32_t *>(a.p.k_codes + at * 128)[lane];
-    const uint32_t vw = reinterpret_cast<const uint32_t *>(a.p.v_codes + at * 128)[lane];
-    const __half ks = __ushort_as_half(a.p.k_scales[at]), vs = __ushort_as_half(a.p.v_scales[at]);
-    float s = 0.f, v[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      s += q[t] * __half2float(__hmul(__int2half_rn(static_cast<int8_t>(kw >> (8 * t))), ks));
-      v[t] = __half2float(__hmul(__int2half_rn(static_cast<int8_t>(vw >> (8 * t))), vs));
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float c = m == -INFINITY ? 0.f : ex2(m - mn), p = mn == -INFINITY ? 0.f : ex2(s - mn);
-    l = l * c + p;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = o[t] * c + p * v[t];
+  const Counts c = counts_of(a, lo);
+  if (c.units == 0 || row < c.q_base || row >= c.q_base + c.nodes) return;
+  const Workspace ws = workspace_of(a);
+  const int64_t total = ws.prefix[a.seqs];
+  const int head = h / a.group;
+  const int x = static_cast<int>(row - c.q_base) * a.group + (h - head * a.group);
+  const int rt = x / kItemRows, r = x - rt * kItemRows;
+  const int64_t u0 = ws.prefix[lo] + (static_cast<int64_t>(head) * c.row_tiles + rt) * c.tiles, u1 = u0 + c.tiles;
+  // the CTA that holds unit u: the last with first_unit <= u
+  const int ctas = working(a, total);
+  auto owner = [&](int64_t u) {
+    int k = static_cast<int>(u * ctas / total);
+    while (k + 1 < ctas && first_unit(total, k + 1, ctas) <= u) ++k;
+    while (k > 0 && first_unit(total, k, ctas) > u) --k;
+    return k;
+  };
+  const int first = owner(u0), last = owner(u1 - 1);
+  if (first == last) return;  // written by the attention kernel
+  float m = kNoMax, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k = first; k <= last; ++k) {
+    const int64_t at = (static_cast<int64_t>(k) * 2 + (k == first ? 1 : 0)) * ws.rows + r;
+    const float2 ml = ws.ml[at];
+    const float4 p = reinterpret_cast<const float4 *>(ws.o + at * 128)[lane];
+    const float mn = fmaxf(m, ml.x);
+    const float ga = ex2((m - mn) * a.scale_log2), gb = ex2((ml.x - mn) * a.scale_log2);
+    l = fmaf(l, ga, ml.y * gb);
+    o[0] = fmaf(o[0], ga, p.x * gb);
+    o[1] = fmaf(o[1], ga, p.y * gb);
+    o[2] = fmaf(o[2], ga, p.z * gb);
+    o[3] = fmaf(o[3], ga, p.w * gb);
     m = mn;
   }
   fwht128_warp(o, lane);
   const float inv = kInvSqrt128 / l;
   *reinterpret_cast<uint2 *>(a.o.data + h * a.o.head_stride + row * a.o.row_stride + 4 * lane) =
       make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  if (a.lse && lane == 0) a.lse[h * a.nodes + row] = 0.6931471805599453f * (m + log2f(l));
+  if (a.lse && lane == 0) a.lse[h * a.nodes + row] = kLn2 * (m * a.scale_log2 + log2f(l));
 }
 
 }  // namespace
+}  // namespace serve
 
-size_t tree_workspace_bytes(int32_t, int32_t, int64_t, int32_t) { return 16; }
+size_t tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs) {
+  const size_t parts = static_cast<size_t>(serve::kMaxCtas) * 2 * serve::part_rows(q_heads / kv_heads, nodes);
+  return serve::prefix_bytes(seqs) + parts * (128 * sizeof(float) + sizeof(float2));
+}
 
-cudaError_t launch_attend_tree(const TreeArgs &a, cudaStream_t stream) {
+cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
+  using namespace serve;
+  TreeArgs a = args;
+  a.ctas = a.ctas < kMaxCtas ? a.ctas : kMaxCtas;
+  cudaError_t e =
+      cudaFuncSetAttribute(tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  if (e != cudaSuccess) return e;
+  tree_kernel<<<a.ctas, kThreads, kSmemBytes, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t units = a.nodes * a.q_heads;
-  tree_kernel<<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(a);
+  join_kernel<<<static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

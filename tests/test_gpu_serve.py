@@ -452,6 +452,18 @@ def test_tree_same_bits_again(cuda):
     b.sync_status()
 
 
+def test_tree_workspace_holds_anything(cuda):
+    # fewer units of work than CTAs, a workspace full of NaN
+    st, ref = random_store(20, 2, 64)
+    q = normal(1, 4, 1, 128)
+    t = [list(range(16))]
+    ws = torch.full((int(b.h3kv_attend_tree_workspace_bytes(4, 2, 1, 1)),), 255, dtype=torch.uint8, device=DEV)
+    out = b.attend_tree(q.to(DEV), st, i32_2d(t), i32([1000]), i32([0, 1]), workspace=ws)
+    b.sync_status()
+    want = so.attend_tree(q, ref, t, [1000], [0, 1])
+    within(out, want[0], want[2], "workspace")
+
+
 def test_tree_rows_behind_the_length_do_not_reach(cuda):
     # what the free rows of the last page, and pages of others, hold
     st, _ = random_store(4, 2, 64)
