@@ -490,29 +490,35 @@ def _need_strided(t, name: str, heads: int | None = None, rows: int | None = Non
     output [rows, heads, 128] is passed as its transpose(0, 1))."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [heads, rows, {HEAD_DIM}]")
-    if heads is not None and t.shape[0] != heads:
-        raise ValueError(f"{name}: {t.shape[0]} heads, expected {heads}")
-    if rows is not None and t.shape[1] != rows:
-        raise ValueError(f"{name}: {t.shape[1]} rows, expected {rows}")
-    if t.numel():
-        if t.stride(2) != 1:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [heads, rows, {HEAD_DIM}]")
+    h, r, _ = shape
+    if heads is not None and h != heads:
+        raise ValueError(f"{name}: {h} heads, expected {heads}")
+    if rows is not None and r != rows:
+        raise ValueError(f"{name}: {r} rows, expected {rows}")
+    hs, rs, inner = t.stride()
+    ptr = t.data_ptr()
+    if h and r:
+        if inner != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        for d in (0, 1):
-            if t.shape[d] > 1 and (t.stride(d) % 8 != 0 or t.stride(d) < HEAD_DIM):
-                raise ValueError(f"{name}: stride {t.stride(d)} of dimension {d} must be a multiple of 8, "
-                                 f"at least {HEAD_DIM}")
-        if t.data_ptr() % 16 != 0:
+        for d, n, st in ((0, h, hs), (1, r, rs)):
+            if n > 1 and (st % 8 != 0 or st < HEAD_DIM):
+                raise ValueError(f"{name}: stride {st} of dimension {d} must be a multiple of 8, at least {HEAD_DIM}")
+        if ptr % 16 != 0:
             raise ValueError(f"{name}: must be 16-byte aligned")
     # the stride of a dimension of one entry is never used
-    return h3kv_rows(_ptr(t), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return h3kv_rows(ptr, hs if h > 1 else 0, rs if r > 1 else 0)
 
 
-def _need_index(t, name: str, shape=None) -> None:
-    _need(t, name, torch.int32, shape)
+def _need_index(t, name: str, shape=None, dtype=torch.int32) -> None:
+    # (the long way round only for the message of a refusal)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        _need(t, name, dtype, shape)
 
 
 def _need_apart(out, **inputs) -> None:
@@ -534,19 +540,49 @@ def _need_apart(out, **inputs) -> None:
             raise ValueError(f"out: shares memory with {name}")
 
 
-@contextlib.contextmanager
-def _device_of(stream, **tensors):
-    """Every tensor of a call on one CUDA device (and the stream too), which
-    is made current for the call."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) != 1 or next(iter(devs)).type != "cuda":
-        where = ", ".join(f"{k} on {t.device}" for k, t in tensors.items() if t is not None)
-        raise ValueError(f"tensors must lie on one CUDA device: {where}")
-    dev = next(iter(devs))
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream of {stream.device}, tensors on {dev}")
-    with torch.cuda.device(dev):
-        yield dev
+def _one_device(stream, tensors: dict) -> int:
+    """The index of the CUDA device that every tensor of a call (and the
+    stream) is on."""
+    dev = None
+    for t in tensors.values():
+        if t is not None:
+            d = t.get_device()
+            dev = d if dev is None else dev
+            if d != dev or d < 0:
+                where = ", ".join(f"{k} on {x.device}" for k, x in tensors.items() if x is not None)
+                raise ValueError(f"tensors must lie on one CUDA device: {where}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
+    return dev
+
+
+# The current stream's handle without building a Stream object (a tenth of the
+# time of torch.cuda.current_stream), where this PyTorch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(dev: int, stream, where: str, fn, *args) -> None:
+    """fn(*args, stream handle) with `dev` as the current device."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, where, fn, *args)
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    status = fn(*args, handle)
+    if status != H3KV_OK:
+        raise H3kvError(status, where)
+
+
+def _new(stream, shape, dtype, dev: int) -> torch.Tensor:
+    """A tensor of a call, allocated on the call's stream (see _on)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 class PagedStore:
@@ -564,6 +600,7 @@ class PagedStore:
         self.pages, self.kv_heads, self.page_size = (int(x) for x in k_codes.shape[:3])
         if self.page_size not in PAGE_SIZES:
             raise ValueError(f"page_size {self.page_size}, expected one of {PAGE_SIZES}")
+        self._checked = None
         self.c_struct()
 
     @classmethod
@@ -579,13 +616,21 @@ class PagedStore:
                 "store.v_scales": self.v_scales}
 
     def c_struct(self) -> h3kv_paged_store:
+        """The C struct of the four buffers, checked again whenever one of
+        them is another than at the last call."""
+        ptrs = (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(), self.v_scales.data_ptr())
+        buffers = (self.k_codes, self.v_codes, self.k_scales, self.v_scales)
+        if self._checked is not None and self._checked[0] == ptrs and all(
+                x is y for x, y in zip(self._checked[1], buffers)):
+            return self._checked[2]
         shape = (self.pages, self.kv_heads, self.page_size)
         _need(self.k_codes, "store.k_codes", torch.int8, (*shape, HEAD_DIM))
         _need(self.v_codes, "store.v_codes", torch.int8, (*shape, HEAD_DIM))
         _need(self.k_scales, "store.k_scales", torch.float16, shape)
         _need(self.v_scales, "store.v_scales", torch.float16, shape)
-        return h3kv_paged_store(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scales), _ptr(self.v_scales),
-                                *shape, HEAD_DIM)
+        st = h3kv_paged_store(*ptrs, *shape, HEAD_DIM)
+        self._checked = (ptrs, buffers, st)
+        return st
 
     def nbytes(self) -> int:
         return int(h3kv_paged_store_bytes(self.pages, self.kv_heads, self.page_size, HEAD_DIM))
@@ -595,13 +640,14 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, store: PagedStore, rows: torc
     """h3kv_paged_append: row i of bf16 K, V [kv_heads, n, 128] rotated,
     quantised and written to pool row rows[i] (int32 [n]; negative: left
     out).  No pool row may be named twice."""
-    k, v = _need_strided(K, "K", store.kv_heads), _need_strided(V, "V", store.kv_heads, int(K.shape[1]))
-    n = int(K.shape[1])
+    k = _need_strided(K, "K", store.kv_heads)
+    n = K.shape[1]
+    v = _need_strided(V, "V", store.kv_heads, n)
     _need_index(rows, "rows", (n,))
     st = store.c_struct()
-    with _device_of(stream, K=K, V=V, rows=rows, **store.tensors()):
-        check(h3kv_paged_append(ctypes.byref(k), ctypes.byref(v), _ptr(rows), n, ctypes.byref(st), _stream(stream)),
-              "h3kv_paged_append")
+    dev = _one_device(stream, {"K": K, "V": V, "rows": rows, **store.tensors()})
+    _launch(dev, stream, "h3kv_paged_append", h3kv_paged_append, ctypes.byref(k), ctypes.byref(v), rows.data_ptr(), n,
+            ctypes.byref(st))
 
 
 def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = None, V: torch.Tensor | None = None,
@@ -611,16 +657,19 @@ def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = N
     _need_index(rows, "rows")
     if rows.dim() != 1:
         raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [n]")
-    n = int(rows.shape[0])
+    n = rows.shape[0]
     st = store.c_struct()
-    with _device_of(stream, rows=rows, **store.tensors()) as dev, _on(stream):
-        K = torch.empty((store.kv_heads, n, HEAD_DIM), dtype=torch.bfloat16, device=dev) if K is None else K
-        V = torch.empty((store.kv_heads, n, HEAD_DIM), dtype=torch.bfloat16, device=dev) if V is None else V
+    dev = _one_device(stream, {"rows": rows, "K": K, "V": V, **store.tensors()})
+    given = {"K": K, "V": V}
+    K = _new(stream, (store.kv_heads, n, HEAD_DIM), torch.bfloat16, dev) if K is None else K
+    V = _new(stream, (store.kv_heads, n, HEAD_DIM), torch.bfloat16, dev) if V is None else V
     k, v = _need_strided(K, "K", store.kv_heads, n), _need_strided(V, "V", store.kv_heads, n)
-    _need_apart(K, V=V if V.data_ptr() == K.data_ptr() else None, rows=rows)
-    with _device_of(stream, K=K, V=V, rows=rows, **store.tensors()):
-        check(h3kv_paged_read(ctypes.byref(st), _ptr(rows), n, ctypes.byref(k), ctypes.byref(v), _stream(stream)),
-              "h3kv_paged_read")
+    for t in given.values():
+        _need_apart(t, rows=rows, **store.tensors())
+    if given["K"] is not None and given["V"] is not None and k.data == v.data and n and store.kv_heads:
+        raise ValueError("out: K shares memory with V")
+    _launch(dev, stream, "h3kv_paged_read", h3kv_paged_read, ctypes.byref(st), rows.data_ptr(), n, ctypes.byref(k),
+            ctypes.byref(v))
     return K, V
 
 
@@ -633,16 +682,16 @@ def paged_copy(store: PagedStore, src: torch.Tensor, dst: torch.Tensor, stream=N
         raise ValueError(f"src: shape {tuple(src.shape)}, expected [n]")
     _need_index(dst, "dst", src.shape)
     st = store.c_struct()
-    with _device_of(stream, src=src, dst=dst, **store.tensors()):
-        check(h3kv_paged_copy(ctypes.byref(st), _ptr(src), _ptr(dst), int(src.shape[0]), _stream(stream)),
-              "h3kv_paged_copy")
+    dev = _one_device(stream, {"src": src, "dst": dst, **store.tensors()})
+    _launch(dev, stream, "h3kv_paged_copy", h3kv_paged_copy, ctypes.byref(st), src.data_ptr(), dst.data_ptr(),
+            src.shape[0])
 
 
 def _need_table(page_table, lengths, cu_nodes) -> int:
     _need_index(cu_nodes, "cu_nodes")
     if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
         raise ValueError(f"cu_nodes: shape {tuple(cu_nodes.shape)}, expected [seqs + 1]")
-    seqs = int(cu_nodes.shape[0]) - 1
+    seqs = cu_nodes.shape[0] - 1
     _need_index(lengths, "lengths", (seqs,))
     _need_index(page_table, "page_table")
     if page_table.dim() != 2 or page_table.shape[0] != seqs:
@@ -657,25 +706,22 @@ def paged_keep(store: PagedStore, page_table: torch.Tensor, lengths: torch.Tenso
     up behind the rows before them, in order -> the lengths that are left
     (int32 [seqs]).  The pages of those rows belong to that sequence alone."""
     seqs = _need_table(page_table, lengths, cu_nodes)
-    _need(keep, "keep", torch.bool if isinstance(keep, torch.Tensor) and keep.dtype == torch.bool else torch.uint8)
-    if keep.dim() != 1:
-        raise ValueError(f"keep: shape {tuple(keep.shape)}, expected [nodes]")
+    if not (isinstance(keep, torch.Tensor) and keep.dtype is torch.bool):
+        _need_index(keep, "keep", dtype=torch.uint8)
+    if keep.dim() != 1 or not keep.is_contiguous():
+        raise ValueError(f"keep: shape {tuple(keep.shape)}, expected contiguous [nodes]")
     st = store.c_struct()
-    with _device_of(stream, page_table=page_table, lengths=lengths, cu_nodes=cu_nodes, keep=keep, out=out,
-                    **store.tensors()) as dev:
-        with _on(stream):
-            out = torch.empty((seqs,), dtype=torch.int32, device=dev) if out is None else out
+    dev = _one_device(stream, {"page_table": page_table, "lengths": lengths, "cu_nodes": cu_nodes, "keep": keep,
+                               "out": out, **store.tensors()})
+    if out is None:
+        out = _new(stream, (seqs,), torch.int32, dev)
+    else:
         _need_index(out, "out", (seqs,))
         _need_apart(out, lengths=lengths, cu_nodes=cu_nodes, page_table=page_table, keep=keep)
-        check(h3kv_paged_keep(ctypes.byref(st), _ptr(page_table), int(page_table.shape[1]), _ptr(lengths),
-                              _ptr(cu_nodes), seqs, _ptr(keep), int(keep.shape[0]), _ptr(out), _stream(stream)),
-              "h3kv_paged_keep")
+    _launch(dev, stream, "h3kv_paged_keep", h3kv_paged_keep, ctypes.byref(st), page_table.data_ptr(),
+            page_table.shape[1], lengths.data_ptr(), cu_nodes.data_ptr(), seqs, keep.data_ptr(), keep.shape[0],
+            out.data_ptr())
     return out
-
-
-def _need_lse(lse, Q) -> None:
-    if lse is not None:
-        _need(lse, "lse", torch.float32, Q.shape[:2])
 
 
 def attend_tree(Q: torch.Tensor, store: PagedStore, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -691,28 +737,30 @@ def attend_tree(Q: torch.Tensor, store: PagedStore, page_table: torch.Tensor, le
     log-sum-exp of the scores.  ``workspace`` (uint8, >=
     h3kv_attend_tree_workspace_bytes) is created here if not given."""
     q = _need_strided(Q, "Q")
-    heads, nodes = int(Q.shape[0]), int(Q.shape[1])
+    heads, nodes, _ = Q.shape
     if store.kv_heads < 1 or heads % store.kv_heads != 0:
         raise ValueError(f"Q: {heads} heads, not a multiple of the store's {store.kv_heads}")
     seqs = _need_table(page_table, lengths, cu_nodes)
     if parents is not None:
         _need_index(parents, "parents", (nodes,))
-    _need_lse(lse, Q)
+    if lse is not None:
+        _need_index(lse, "lse", (heads, nodes), torch.float32)
     st = store.c_struct()
-    with _device_of(stream, Q=Q, page_table=page_table, lengths=lengths, cu_nodes=cu_nodes, parents=parents, out=out,
-                    lse=lse, workspace=workspace, **store.tensors()) as dev:
-        need = int(h3kv_attend_tree_workspace_bytes(heads, store.kv_heads, nodes, seqs))
-        with _on(stream):
-            out = torch.empty((heads, nodes, HEAD_DIM), dtype=torch.bfloat16, device=dev) if out is None else out
-            if workspace is None:
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        o = _need_strided(out, "out", heads, nodes)
-        _need(workspace, "workspace", torch.uint8)
+    dev = _one_device(stream, {"Q": Q, "page_table": page_table, "lengths": lengths, "cu_nodes": cu_nodes,
+                               "parents": parents, "out": out, "lse": lse, "workspace": workspace, **store.tensors()})
+    given = out is not None
+    out = out if given else _new(stream, (heads, nodes, HEAD_DIM), torch.bfloat16, dev)
+    o = _need_strided(out, "out", heads, nodes)
+    if workspace is None:
+        need = h3kv_attend_tree_workspace_bytes(heads, store.kv_heads, nodes, seqs)
+        workspace = _new(stream, (max(need, 16),), torch.uint8, dev)
+    else:
+        _need_index(workspace, "workspace", dtype=torch.uint8)
+    if given:
         _need_apart(out, Q=Q, lse=lse, workspace=workspace)
-        check(h3kv_attend_tree(ctypes.byref(q), heads, nodes, ctypes.byref(st), _ptr(page_table),
-                               int(page_table.shape[1]), _ptr(lengths), _ptr(cu_nodes), seqs, _ptr(parents),
-                               float(softmax_scale), ctypes.byref(o), _ptr(lse), _ptr(workspace), workspace.numel(),
-                               _stream(stream)), "h3kv_attend_tree")
+    _launch(dev, stream, "h3kv_attend_tree", h3kv_attend_tree, ctypes.byref(q), heads, nodes, ctypes.byref(st),
+            page_table.data_ptr(), page_table.shape[1], lengths.data_ptr(), cu_nodes.data_ptr(), seqs, _ptr(parents),
+            softmax_scale, ctypes.byref(o), _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -725,8 +773,9 @@ def attend_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch
     bf16 like Q.  ``lse`` (fp32 [q_heads, q_rows]) takes the log-sum-exp of
     the scores.  Rows of no sequence are left as they are in ``out``."""
     q, k = _need_strided(Q, "Q"), _need_strided(K, "K")
-    heads, kv_heads, rows = int(Q.shape[0]), int(K.shape[0]), int(Q.shape[1])
-    v = _need_strided(V, "V", kv_heads, int(K.shape[1]))
+    heads, rows, _ = Q.shape
+    kv_heads, k_rows, _ = K.shape
+    v = _need_strided(V, "V", kv_heads, k_rows)
     if kv_heads < 1 or heads % kv_heads != 0:
         raise ValueError(f"Q: {heads} heads, not a multiple of K's {kv_heads}")
     _need_index(cu_q, "cu_q")
@@ -734,16 +783,17 @@ def attend_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch
         raise ValueError(f"cu_q: shape {tuple(cu_q.shape)}, expected [seqs + 1]")
     cu_k = cu_q if cu_k is None else cu_k
     _need_index(cu_k, "cu_k", cu_q.shape)
-    _need_lse(lse, Q)
-    with _device_of(stream, Q=Q, K=K, V=V, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse) as dev:
-        with _on(stream):
-            out = torch.empty((heads, rows, HEAD_DIM), dtype=torch.bfloat16, device=dev) if out is None else out
-        o = _need_strided(out, "out", heads, rows)
+    if lse is not None:
+        _need_index(lse, "lse", (heads, rows), torch.float32)
+    dev = _one_device(stream, {"Q": Q, "K": K, "V": V, "cu_q": cu_q, "cu_k": cu_k, "out": out, "lse": lse})
+    given = out is not None
+    out = out if given else _new(stream, (heads, rows, HEAD_DIM), torch.bfloat16, dev)
+    o = _need_strided(out, "out", heads, rows)
+    if given:
         _need_apart(out, Q=Q, K=K, V=V, lse=lse)
-        check(h3kv_attend_prompt(ctypes.byref(q), heads, rows, ctypes.byref(k), ctypes.byref(v), kv_heads,
-                                 int(K.shape[1]), _ptr(cu_q), _ptr(cu_k), int(cu_q.shape[0]) - 1, int(bool(causal)),
-                                 float(softmax_scale), ctypes.byref(o), _ptr(lse), _stream(stream)),
-              "h3kv_attend_prompt")
+    _launch(dev, stream, "h3kv_attend_prompt", h3kv_attend_prompt, ctypes.byref(q), heads, rows, ctypes.byref(k),
+            ctypes.byref(v), kv_heads, k_rows, cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, bool(causal),
+            softmax_scale, ctypes.byref(o), _ptr(lse))
     return out
 
 

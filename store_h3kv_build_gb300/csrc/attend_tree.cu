@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Workspace ws = workspace_of(a);
 
+  // the join may start its CTAs; it waits there until this grid is done
+  if (tid == 0) pdl_launch_dependents();
   // units of all sequences, then the sequence that holds this CTA's first one
   int64_t mine = 0;
   for (int i = tid; i < a.seqs; i += kThreads) {
@@ -210,23 +212,43 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const int r = base_row + i;
       const int w0 = base_row + (warp & 3) * 32;  // the warp's first row
       const bool warp_on = w0 < s.rows;
-      // q' = fp16(q H): the warp's rows one at a time, rotated across the warp,
-      // into the swizzled K-major tile.  The tile is free: this stream's last
-      // QK of the segment before has completed.
+      // q' = fp16(q H) into the swizzled K-major tile, which is free: this
+      // stream's last QK of the segment before has completed.  8 lanes hold a
+      // row (values 8l .. 8l+7 and 64 + 8l .. of it), the warp 4 rows at a
+      // time; all of its rows' loads go out before the first is used.
       if (has_tiles(s, q)) {
-        const int n = s.rows - w0 < 32 ? s.rows - w0 : 32;
-        for (int rr = 0; rr < n; ++rr) {
-          const int x = s.row0 + w0 + rr, node = x / a.group;
-          const int h = s.head * a.group + (x - node * a.group);
-          const uint2 raw = *(reinterpret_cast<const uint2 *>(a.q.data + h * a.q.head_stride +
-                                                              (s.q_base + node) * a.q.row_stride) +
-                              lane);
-          float v[4] = {bf16lo_to_f32(raw.x), bf16hi_to_f32(raw.x), bf16lo_to_f32(raw.y), bf16hi_to_f32(raw.y)};
-          fwht128_warp(v, lane);
-          *reinterpret_cast<uint2 *>(sm.q[q] + (lane >> 4) * kChunkBytes +
-                                     sw128_off((warp & 3) * 32 + rr, (lane & 15) >> 1) + (lane & 1) * 8) =
-              make_uint2(pack_f16x2(v[0] * kInvSqrt128, v[1] * kInvSqrt128),
-                         pack_f16x2(v[2] * kInvSqrt128, v[3] * kInvSqrt128));
+        if (warp_on) {
+          const int l = lane & 7;
+          uint4 raw[8][2];
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int rr = it * 4 + (lane >> 3);
+            raw[it][0] = raw[it][1] = make_uint4(0, 0, 0, 0);
+            if (w0 + rr < s.rows) {
+              const int x = s.row0 + w0 + rr, node = x / a.group, h = s.head * a.group + (x - node * a.group);
+              const uint4 *src = reinterpret_cast<const uint4 *>(a.q.data + h * a.q.head_stride +
+                                                                 (s.q_base + node) * a.q.row_stride) +
+                                 l;
+              raw[it][0] = __ldg(src);
+              raw[it][1] = __ldg(src + 8);
+            }
+          }
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            if (w0 + it * 4 >= s.rows) break;
+            const int rr = (warp & 3) * 32 + it * 4 + (lane >> 3);
+            float v[16];
+            unpack_bf16x8(raw[it][0], v);
+            unpack_bf16x8(raw[it][1], v + 8);
+            fwht128_oct(v, l);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= kInvSqrt128;
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi)
+              *reinterpret_cast<uint4 *>(sm.q[q] + hi * kChunkBytes + sw128_off(rr, l)) =
+                  make_uint4(pack_f16x2(v[8 * hi], v[8 * hi + 1]), pack_f16x2(v[8 * hi + 2], v[8 * hi + 3]),
+                             pack_f16x2(v[8 * hi + 4], v[8 * hi + 5]), pack_f16x2(v[8 * hi + 6], v[8 * hi + 7]));
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -431,16 +453,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a)
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int64_t row = unit / a.q_heads;
   const int h = static_cast<int>(unit - row * a.q_heads);
-  if (row >= a.nodes) return;
-  int lo = 0, hi = a.seqs;
+  int lo = 0, hi = row < a.nodes ? a.seqs : 0;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(a.cu_nodes + mid + 1) <= row) lo = mid + 1;
     else hi = mid;
   }
-  if (lo == a.seqs) return;
-  const Counts c = counts_of(a, lo);
-  if (c.units == 0 || row < c.q_base || row >= c.q_base + c.nodes) return;
+  const bool live = row < a.nodes && lo < a.seqs;
+  Counts c = {};
+  if (live) c = counts_of(a, lo);
+  // (no thread leaves before this, so the grids end in stream order)
+  pdl_wait_prerequisites();
+  if (!live || c.units == 0 || row < c.q_base || row >= c.q_base + c.nodes) return;
   const Workspace ws = workspace_of(a);
   const int64_t total = ws.prefix[a.seqs];
   const int head = h / a.group;
@@ -496,8 +520,16 @@ cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
   tree_kernel<<<a.ctas, kThreads, kSmemBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t units = a.nodes * a.q_heads;
-  join_kernel<<<static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, a);
 }
 
 }  // namespace h3kv

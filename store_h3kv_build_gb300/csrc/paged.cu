@@ -4,40 +4,13 @@
 // All four are bound by HBM at size and by latency for a decoding step's few
 // rows; none has arithmetic worth a tensor core.
 #include "ptx.cuh"
-#include "serve.h"
+#include "serve_rows.cuh"
 
 namespace h3kv {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsPerCta = kThreads / 8;
-
-// Unnormalised FWHT of a 128-value row held by 8 neighbouring lanes: value
-// 64 hi + 8 l + e of the row is x[8 hi + e] of the group's lane l, so that a
-// row's loads and stores are two runs of 8 lanes x 16 bytes.  Strides 1, 2, 4
-// and 64 run in registers, strides 8, 16, 32 between lanes: 48 shuffles for
-// the warp's 4 rows, against 80 with a row across the warp.
-__device__ __forceinline__ void fwht128_oct(float (&x)[16], int l) {
-#pragma unroll
-  for (int h = 1; h < 16; h <<= 1) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if ((i & h) == 0) {
-        const float a = x[i], b = x[i + h];
-        x[i] = a + b;
-        x[i + h] = a - b;
-      }
-    }
-  }
-#pragma unroll
-  for (int m = 1; m < 8; m <<= 1) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
-      x[i] = (l & m) ? o - x[i] : x[i] + o;
-    }
-  }
-}
 
 // Pool row `r` -> its row in [pages, kv_heads, page_size].
 __device__ __forceinline__ int64_t pool_row(const PagedArgs &p, int32_t r, int32_t head) {
@@ -86,10 +59,9 @@ __global__ void __launch_bounds__(kThreads)
     lo = __ldcs(src);
     hi = __ldcs(src + 8);
   }
-  float x[16] = {bf16lo_to_f32(lo.x), bf16hi_to_f32(lo.x), bf16lo_to_f32(lo.y), bf16hi_to_f32(lo.y),
-                 bf16lo_to_f32(lo.z), bf16hi_to_f32(lo.z), bf16lo_to_f32(lo.w), bf16hi_to_f32(lo.w),
-                 bf16lo_to_f32(hi.x), bf16hi_to_f32(hi.x), bf16lo_to_f32(hi.y), bf16hi_to_f32(hi.y),
-                 bf16lo_to_f32(hi.z), bf16hi_to_f32(hi.z), bf16lo_to_f32(hi.w), bf16hi_to_f32(hi.w)};
+  float x[16];
+  unpack_bf16x8(lo, x);
+  unpack_bf16x8(hi, x + 8);
   // 2^-7 first (exact), so that a sum of 128 of the largest bf16 values stays
   // finite; the values that it makes subnormal lie far below the least scale
 #pragma unroll
@@ -100,12 +72,18 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]));
 #pragma unroll
   for (int m = 1; m < 8; m <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
-  // s = fp16(absmax(x H) / 127), saturated; codes rne(x H / s) with the stored s
-  constexpr float kNorm = kInvSqrt128 * 128.0f;
-  __half s = __float2half_rn(a * kNorm / 127.0f);
+  // s = fp16(absmax(x H) / 127), saturated; codes rne(x H / s) with the stored s.
+  // absmax * sqrt(128) / 127 in two fp32 parts p + e: where p alone lies on
+  // the tie between two fp16 values, e says which side the product is on.
+  constexpr float kHi = 0.08908431977033615f, kLo = -8.806923523785315e-10f;  // sqrt(128) / 127
+  float scale = a * kHi;
+  const float e = fmaf(a, kLo, fmaf(a, kHi, -scale));
+  uint32_t bits = __float_as_uint(scale);
+  if ((bits & 0x1FFFu) == 0x1000u) scale = __uint_as_float(bits + (e > 0.f ? 1 : e < 0.f ? -1 : 0));
+  __half s = __float2half_rn(scale);
   if (__hisinf(s)) s = __ushort_as_half(0x7BFFu);
   const float sf = __half2float(s);
-  const float m = sf > 0.f ? kNorm / sf : 0.f;
+  const float m = sf > 0.f ? kInvSqrt128 * 128.0f / sf : 0.f;
   if (r >= 0) {
     const int64_t at = pool_row(p, r, w.head);
     uint2 *dst = reinterpret_cast<uint2 *>((w.v ? p.v_codes : p.k_codes) + at * 128) + l;

@@ -27,7 +27,7 @@
 #include <math.h>
 
 #include "attend.cuh"
-#include "serve.h"
+#include "serve_rows.cuh"
 
 namespace h3kv {
 namespace serve {

@@ -1,0 +1,48 @@
+// serve_rows.cuh -- rows of 128 values held by 8 lanes, as the serving operators
+// read, rotate and write them.
+#pragma once
+
+#include "ptx.cuh"
+#include "serve.h"
+
+namespace h3kv {
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 w, float *x) {
+  x[0] = bf16lo_to_f32(w.x);
+  x[1] = bf16hi_to_f32(w.x);
+  x[2] = bf16lo_to_f32(w.y);
+  x[3] = bf16hi_to_f32(w.y);
+  x[4] = bf16lo_to_f32(w.z);
+  x[5] = bf16hi_to_f32(w.z);
+  x[6] = bf16lo_to_f32(w.w);
+  x[7] = bf16hi_to_f32(w.w);
+}
+
+// Unnormalised FWHT of a 128-value row held by 8 neighbouring lanes: value
+// 64 hi + 8 l + e of the row is x[8 hi + e] of the group's lane l, so that a
+// row's loads and stores are two runs of 8 lanes x 16 bytes.  Strides 1, 2, 4
+// and 64 run in registers, strides 8, 16, 32 between lanes: 48 shuffles for
+// the warp's 4 rows, against 80 with a row across the warp.
+__device__ __forceinline__ void fwht128_oct(float (&x)[16], int l) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if ((i & h) == 0) {
+        const float a = x[i], b = x[i + h];
+        x[i] = a + b;
+        x[i + h] = a - b;
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
+      x[i] = (l & m) ? o - x[i] : x[i] + o;
+    }
+  }
+}
+
+}  // namespace h3kv
