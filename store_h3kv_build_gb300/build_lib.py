@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libh3kv.so")
 SOURCES = ["abi.cu", "store_build.cu", "attend_kvi8r.cu", "attend_exact.cu", "attend_static_scratch.cu",
            "store_f8.cu", "attend_f8.cu", "store_fp4.cu", "attend_fp4.cu",
-           "serve_abi.cu", "paged.cu", "attend_tree.cu", "attend_prompt.cu"]
+           "serve_abi.cu", "paged.cu", "attend_tree.cu", "attend_tree_few.cu", "attend_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-Xptxas", "-v", "-I", os.path.join(os.path.dirname(HERE), "include")]

@@ -1,188 +1,28 @@
-// attend_tree.cu -- attention of drafted tokens over the paged kvi8r cache (the
-// pipeline of serve_attend.cuh), keys split evenly over the SMs.
-//
-// The work is the list of all (sequence, kv head, 256-row tile, 128-key tile)
-// units in that order.  One CTA per SM takes an equal run of it, whatever the
-// lengths: a segment is the part of a run that belongs to one (sequence, head,
-// row tile).  A segment that holds every key tile of its rows writes the
-// output; the others write their un-normalised output with (max, sum) to the
-// workspace, and a second kernel joins each row's parts in order.  A CTA has at
-// most two such parts: the end of an item begun before its run, and the
-// beginning of one that goes on behind it.
-#include "serve_attend.cuh"
+// attend_tree.cu -- attention of drafted tokens over the paged kvi8r cache: the
+// kernel for many rows of a sequence and kv head (the tcgen05 pipeline of
+// serve_attend.cuh), the join, and the choice of kernel.
+#include "tree.cuh"
 
 namespace h3kv {
 namespace serve {
 namespace {
 
-constexpr int kMaxCtas = 152;
-constexpr int kItemRows = 2 * kBM;
-
-// Workspace: prefix of units before each sequence (int64 [seqs + 1]), then
-// per CTA and part (max, sum) [rows] and un-normalised O [rows][128].
-struct Workspace {
-  int64_t *prefix;
-  float2 *ml;
-  float *o;
-  int rows;  // rows of a part
+struct TreeSmem : Smem {
+  Scan scan;
 };
-__host__ __device__ inline int part_rows(int group, int64_t nodes) {
-  const int64_t n = group * (nodes < H3KV_TREE_MAX_NODES ? nodes : H3KV_TREE_MAX_NODES);
-  return n < kItemRows ? static_cast<int>(n) : kItemRows;
-}
-__host__ __device__ inline size_t prefix_bytes(int32_t seqs) {
-  return (static_cast<size_t>(seqs + 1) * 8 + 255) / 256 * 256;
-}
-__device__ inline Workspace workspace_of(const TreeArgs &a) {
-  Workspace ws;
-  uint8_t *p = reinterpret_cast<uint8_t *>(a.workspace);
-  ws.rows = part_rows(a.group, a.nodes);
-  ws.prefix = reinterpret_cast<int64_t *>(p);
-  ws.o = reinterpret_cast<float *>(p + prefix_bytes(a.seqs));
-  ws.ml = reinterpret_cast<float2 *>(ws.o + static_cast<int64_t>(a.ctas) * 2 * ws.rows * 128);
-  return ws;
-}
-
-// A sequence's counts; tiles == 0: nothing to do (empty, or out of range).
-struct Counts {
-  int64_t q_base;
-  int32_t len, nodes, tiles, row_tiles;
-  int64_t units;
-  bool bad;
-};
-__device__ __forceinline__ Counts counts_of(const TreeArgs &a, int i) {
-  const int64_t c0 = __ldg(a.cu_nodes + i), c1 = __ldg(a.cu_nodes + i + 1), len = __ldg(a.lengths + i), m = c1 - c0;
-  Counts c;
-  c.bad = c0 < 0 || m < 0 || c1 > a.nodes || m > H3KV_TREE_MAX_NODES || len < m ||
-          len > (a.max_pages << a.p.page_shift) || len > INT32_MAX - 256;
-  const bool on = !c.bad && m > 0;
-  c.q_base = c0;
-  c.len = on ? static_cast<int32_t>(len) : 0;
-  c.nodes = on ? static_cast<int32_t>(m) : 0;
-  c.tiles = (c.len + kBN - 1) / kBN;
-  c.row_tiles = (c.nodes * a.group + kItemRows - 1) / kItemRows;
-  c.units = static_cast<int64_t>(c.tiles) * c.row_tiles * a.p.kv_heads;
-  return c;
-}
-
-// CTAs that get work, each at least one unit, and the first unit of one.
-__device__ __forceinline__ int working(const TreeArgs &a, int64_t total) {
-  return total < a.ctas ? static_cast<int>(total) : a.ctas;
-}
-__device__ __forceinline__ int64_t first_unit(int64_t total, int cta, int ctas) { return total * cta / ctas; }
-
-// The segments of a run of units, one after the other.  Every role walks its
-// own copy.
-struct Walk {
-  int64_t u, end;     // units left: [u, end)
-  int64_t before;     // units before sequence `seq`
-  int seq;
-  Counts c;
-  __device__ __forceinline__ void start(const TreeArgs &a, const Smem &sm, int64_t u0, int64_t u1) {
-    u = u0;
-    end = u1;
-    seq = sm.scan_seq;
-    before = sm.scan_prefix;
-    if (u < end) c = counts_of(a, seq);
-  }
-  __device__ __forceinline__ bool next(const TreeArgs &a, Seg *s) {
-    if (u >= end) return false;
-    while (u >= before + c.units) {
-      before += c.units;
-      c = counts_of(a, ++seq);
-    }
-    const int64_t w = u - before, item = w / c.tiles;
-    s->t0 = static_cast<int>(w - item * c.tiles);
-    const int64_t left = end - u;
-    s->n = c.tiles - s->t0 < left ? c.tiles - s->t0 : static_cast<int>(left);
-    s->n0 = s->n;
-    s->head = static_cast<int>(item / c.row_tiles);
-    s->row0 = static_cast<int>(item - static_cast<int64_t>(s->head) * c.row_tiles) * kItemRows;
-    const int rows = c.nodes * a.group - s->row0;
-    s->rows = rows < kItemRows ? rows : kItemRows;
-    s->two = s->rows > kBM;
-    s->keys = c.len;
-    s->q_base = c.q_base;
-    s->k_base = static_cast<int64_t>(seq) * a.max_pages;
-    s->nodes = c.nodes;
-    s->seq = seq;
-    s->diff = 0;
-    s->whole = s->n == c.tiles;
-    u += s->n;
-    return true;
-  }
-};
-
-// Node j's path to its root as bits.
-__device__ __forceinline__ uint64_t path_of(const TreeArgs &a, int64_t q_base, int j) {
-  if (!a.parents) return (2ull << j) - 1;
-  uint64_t path = 0;
-  for (int n = j; n >= 0;) {
-    path |= 1ull << n;
-    const int up = __ldg(a.parents + q_base + n);
-    n = up >= 0 && up < n ? up : -1;
-  }
-  return path;
-}
-
-// The 128-column mask of a row for the tile at key `pos`: all keys below
-// `base`, and node i's key base + i where bit i of `path` is set.
-__device__ __forceinline__ void tree_mask(int32_t pos, int32_t base, uint64_t path, uint32_t (&see)[4]) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int32_t off = base - (pos + 32 * g);  // columns below off come before the nodes
-    if (off >= 32) see[g] = 0xffffffffu;
-    else if (off >= 0) see[g] = ((1u << off) - 1u) | static_cast<uint32_t>(path << off);
-    else see[g] = off > -64 ? static_cast<uint32_t>(path >> -off) : 0u;
-  }
-}
-
-// The page of the row at token `pos`; a page out of range is reported and
-// page 0 read in its place.
-__device__ __forceinline__ int32_t page_at(const TreeArgs &a, int64_t table, int32_t pos) {
-  const int32_t page = __ldg(a.page_table + table + (pos >> a.p.page_shift));
-  if (page < 0 || page >= a.p.pages) {
-    atomicOr(a.p.err, kErrIndex);
-    return 0;
-  }
-  return page;
-}
+constexpr size_t kTreeSmemBytes = sizeof(TreeSmem) + 1024;
+static_assert(kTreeSmemBytes <= 232448, "shared memory budget");
 
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TreeSmem &sm = *reinterpret_cast<TreeSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Workspace ws = workspace_of(a);
 
   // the join may start its CTAs; it waits there until this grid is done
   if (tid == 0) pdl_launch_dependents();
-  // units of all sequences, then the sequence that holds this CTA's first one
-  int64_t mine = 0;
-  for (int i = tid; i < a.seqs; i += kThreads) {
-    const Counts c = counts_of(a, i);
-    mine += c.units;
-    if (c.bad && blockIdx.x == 0) atomicOr(a.p.err, kErrIndex);
-  }
-  const int64_t total = block_sum(sm, mine);
-  const int ctas = working(a, total), cta = static_cast<int>(blockIdx.x);
-  const int64_t u0 = cta < ctas ? first_unit(total, cta, ctas) : total;
-  const int64_t u1 = cta < ctas ? first_unit(total, cta + 1, ctas) : total;
-  int64_t before = 0;
-  for (int base = 0; base < a.seqs; base += kThreads) {
-    const int i = base + tid;
-    const int64_t n = i < a.seqs ? counts_of(a, i).units : 0;
-    int64_t all;
-    const int64_t at = before + block_prefix(sm, n, &all);
-    if (i < a.seqs && u0 >= at && u0 < at + n) {
-      sm.scan_seq = i;
-      sm.scan_prefix = at;
-    }
-    if (blockIdx.x == 0 && i < a.seqs) ws.prefix[i] = at;
-    before += all;
-    if (cta != 0 && u0 < before) break;
-  }
-  if (blockIdx.x == 0 && tid == 0) ws.prefix[a.seqs] = total;
-  if (u0 >= u1) return;
+  find_run<kThreads>(a, ws, sm.scan);
+  if (sm.scan.u0 >= sm.scan.u1) return;
 
   if (tid == 0) init_barriers(sm, true);
   if (warp == 13) {
@@ -200,7 +40,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   if (warp < 8) {
     // =================================================== softmax warpgroups
     reg_alloc<kRegSoftmax>();
-    walk.start(a, sm, u0, u1);
+    walk.start(a, sm.scan);
     const int q = warp >> 2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + q * 128, tO = tmem + lane_base + 256 + q * 128;
@@ -322,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   } else if (warp < 12) {
     // ======================================================= dequantisers
     reg_dealloc<kRegDequant>();
-    walk.start(a, sm, u0, u1);
+    walk.start(a, sm.scan);
     const int dw = warp - 8;
     const attn::DqOffsets off = attn::dq_offsets(dw, lane);
     const int rr = 2 * (lane >> 4) + ((lane >> 2) & 1);
@@ -358,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     }
   } else {
     reg_dealloc<kRegIssue>();
-    walk.start(a, sm, u0, u1);
+    walk.start(a, sm.scan);
     if (warp == 12) {
       // ========================================================== producer
       // A tile's codes come page by page (lanes 0-7) into the buffer's second
@@ -469,7 +309,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a)
   const int64_t total = ws.prefix[a.seqs];
   const int head = h / a.group;
   const int x = static_cast<int>(row - c.q_base) * a.group + (h - head * a.group);
-  const int rt = x / kItemRows, r = x - rt * kItemRows;
+  const int rt = x / a.item_rows, r = x - rt * a.item_rows;
   const int64_t u0 = ws.prefix[lo] + (static_cast<int64_t>(head) * c.row_tiles + rt) * c.tiles, u1 = u0 + c.tiles;
   // the CTA that holds unit u: the last with first_unit <= u
   const int ctas = working(a, total);
@@ -506,19 +346,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a)
 }  // namespace serve
 
 size_t tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs) {
-  const size_t parts = static_cast<size_t>(serve::kMaxCtas) * 2 * serve::part_rows(q_heads / kv_heads, nodes);
-  return serve::prefix_bytes(seqs) + parts * (128 * sizeof(float) + sizeof(float2));
+  const int32_t group = q_heads / kv_heads;
+  const size_t rows = serve::part_rows(group, nodes, serve::item_rows_of(group, nodes, seqs));
+  return serve::prefix_bytes(seqs) + serve::kMaxCtas * 2 * rows * (128 * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
   using namespace serve;
   TreeArgs a = args;
   a.ctas = a.ctas < kMaxCtas ? a.ctas : kMaxCtas;
-  cudaError_t e =
-      cudaFuncSetAttribute(tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  a.item_rows = item_rows_of(a.group, a.nodes, a.seqs);
+  cudaError_t e;
+  if (a.item_rows < kManyRows) {
+    e = launch_tree_few(a, stream);
+  } else {
+    e = cudaFuncSetAttribute(tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kTreeSmemBytes));
+    if (e != cudaSuccess) return e;
+    tree_kernel<<<a.ctas, kThreads, kTreeSmemBytes, stream>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
-  tree_kernel<<<a.ctas, kThreads, kSmemBytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t units = a.nodes * a.q_heads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps));

@@ -54,11 +54,16 @@ struct TreeArgs {
   float scale_log2;
   float *workspace;
   int32_t ctas;
+  int32_t item_rows;   // rows of a row tile, by the kernel that runs
   uint64_t timeout_ns;
   int32_t withhold_p_tile1;
 };
 size_t tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs);
 cudaError_t launch_attend_tree(const TreeArgs &a, cudaStream_t stream);
+// Its kernel for a.item_rows 8 or 16 (launch_attend_tree adds the join).
+cudaError_t launch_tree_few(const TreeArgs &a, cudaStream_t stream);
+// 2-D map over 8-bit codes [rows, 128]: box 128 x box_rows, 128-byte swizzle.
+bool encode_codes(CUtensorMap *m, const void *base, int64_t rows, uint32_t box_rows);
 
 struct PromptArgs {
   h3kv_rows q, k, v, o;

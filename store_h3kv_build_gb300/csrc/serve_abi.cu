@@ -35,7 +35,9 @@ h3kv_status paged_args(const h3kv_paged_store *st, h3kv::PagedArgs *out) {
   if (st->head_dim != H3KV_HEAD_DIM) return H3KV_ERR_UNSUPPORTED;
   const int32_t ps = st->page_size;
   if (ps != 16 && ps != 32 && ps != 64 && ps != 128) return H3KV_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(st->pages) * ps > kMaxRows) return H3KV_ERR_INVALID_ARG;
+  // row numbers, and rows of all heads, in 31 bits
+  if (static_cast<int64_t>(st->pages) * ps > kMaxRows / (st->kv_heads > 0 ? st->kv_heads : 1))
+    return H3KV_ERR_INVALID_ARG;
   if (st->pages > 0 && st->kv_heads > 0) {
     if (!st->k_codes || !st->v_codes || !st->k_scales || !st->v_scales) return H3KV_ERR_INVALID_ARG;
     if (!aligned(st->k_codes, 16) || !aligned(st->v_codes, 16) || !aligned(st->k_scales, 16) ||

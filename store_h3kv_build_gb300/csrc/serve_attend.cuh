@@ -132,20 +132,6 @@ __device__ __forceinline__ void init_barriers(Smem &sm, bool cache) {
   fence_mbar_init();
 }
 
-// Sum of `v` over the block; every thread gets it.  All threads call it.
-__device__ __forceinline__ int64_t block_sum(Smem &sm, int64_t v) {
-  const int warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm.warp_sum[warp] = v;
-  __syncthreads();
-  int64_t t = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) t += sm.warp_sum[w];
-  return t;
-}
-
 // Sum of the values of the threads before this one, and of all.
 __device__ __forceinline__ int64_t block_prefix(Smem &sm, int64_t v, int64_t *total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -1,0 +1,239 @@
+// tree.cuh -- what the two kernels of h3kv_attend_tree and their join share: how
+// the work is listed and split over the CTAs, the workspace, a node's mask.
+//
+// The work is the list of all (sequence, kv head, row tile, 128-key tile)
+// units in that order.  One CTA per SM takes an equal run of it, whatever the
+// lengths: a segment is the part of a run that belongs to one (sequence, head,
+// row tile).  A segment that holds every key tile of its rows writes the
+// output; the others write their un-normalised output with (max, sum) to the
+// workspace, and a second kernel joins each row's parts in order.  A CTA has at
+// most two such parts: the end of an item begun before its run, and the
+// beginning of one that goes on behind it.
+#pragma once
+
+#include "serve_attend.cuh"
+
+namespace h3kv {
+namespace serve {
+namespace {
+
+constexpr int kMaxCtas = 152;
+
+// Rows of an item (a row tile of one sequence and kv head): 256 on the tcgen05
+// pipeline, 8 or 16 on the few-row kernel.
+constexpr int kManyRows = 256;
+
+// Which of them, by the mean rows of a sequence and kv head (the host does not
+// know the single counts; every kernel is right for all of them).
+inline int item_rows_of(int32_t group, int64_t nodes, int32_t seqs) {
+  const int64_t mean = (group * nodes + seqs - 1) / (seqs > 0 ? seqs : 1);
+  return mean <= 8 ? 8 : mean <= 16 ? 16 : kManyRows;
+}
+
+// Workspace: prefix of units before each sequence (int64 [seqs + 1]), then
+// per CTA and part (max, sum) [rows] and un-normalised O [rows][128].
+struct Workspace {
+  int64_t *prefix;
+  float2 *ml;
+  float *o;
+  int rows;  // rows of a part
+};
+__host__ __device__ inline int part_rows(int group, int64_t nodes, int item_rows) {
+  const int64_t n = group * (nodes < H3KV_TREE_MAX_NODES ? nodes : H3KV_TREE_MAX_NODES);
+  return n < item_rows ? static_cast<int>(n) : item_rows;
+}
+__host__ __device__ inline size_t prefix_bytes(int32_t seqs) {
+  return (static_cast<size_t>(seqs + 1) * 8 + 255) / 256 * 256;
+}
+__device__ inline Workspace workspace_of(const TreeArgs &a) {
+  Workspace ws;
+  uint8_t *p = reinterpret_cast<uint8_t *>(a.workspace);
+  ws.rows = part_rows(a.group, a.nodes, a.item_rows);
+  ws.prefix = reinterpret_cast<int64_t *>(p);
+  ws.o = reinterpret_cast<float *>(p + prefix_bytes(a.seqs));
+  ws.ml = reinterpret_cast<float2 *>(ws.o + static_cast<int64_t>(a.ctas) * 2 * ws.rows * 128);
+  return ws;
+}
+
+// A sequence's counts; tiles == 0: nothing to do (empty, or out of range).
+struct Counts {
+  int64_t q_base;
+  int32_t len, nodes, tiles, row_tiles;
+  int64_t units;
+  bool bad;
+};
+__device__ __forceinline__ Counts counts_of(const TreeArgs &a, int i) {
+  const int64_t c0 = __ldg(a.cu_nodes + i), c1 = __ldg(a.cu_nodes + i + 1), len = __ldg(a.lengths + i), m = c1 - c0;
+  Counts c;
+  c.bad = c0 < 0 || m < 0 || c1 > a.nodes || m > H3KV_TREE_MAX_NODES || len < m ||
+          len > (a.max_pages << a.p.page_shift) || len > INT32_MAX - 256;
+  const bool on = !c.bad && m > 0;
+  c.q_base = c0;
+  c.len = on ? static_cast<int32_t>(len) : 0;
+  c.nodes = on ? static_cast<int32_t>(m) : 0;
+  c.tiles = (c.len + kBN - 1) / kBN;
+  c.row_tiles = (c.nodes * a.group + a.item_rows - 1) / a.item_rows;
+  c.units = static_cast<int64_t>(c.tiles) * c.row_tiles * a.p.kv_heads;
+  return c;
+}
+
+// CTAs that get work, each at least one unit, and the first unit of one.
+__device__ __forceinline__ int working(const TreeArgs &a, int64_t total) {
+  return total < a.ctas ? static_cast<int>(total) : a.ctas;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+
+// This CTA's run of units: found by all threads of the block, kept in shared
+// memory.  CTA 0 also checks every sequence and writes the prefix array.
+struct Scan {
+  int64_t u0, u1;
+  int64_t before;  // units before sequence `seq`, which holds unit u0
+  int seq;
+  int64_t warp_sum[32];
+};
+
+template <int kBlock>
+__device__ __forceinline__ int64_t block_prefix(int64_t (&warp_sum)[32], int64_t v, int64_t *total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t inc = v;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
+    if (lane >= x) inc += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t below = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kBlock / 32; ++w) {
+    const int64_t t = warp_sum[w];
+    below += w < warp ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return below + inc - v;
+}
+
+template <int kBlock>
+__device__ __forceinline__ void find_run(const TreeArgs &a, const Workspace &ws, Scan &sc) {
+  const int tid = threadIdx.x;
+  int64_t total = 0, first = 0;  // first: units of this thread's sequence of the first round
+  for (int base = 0; base < a.seqs; base += kBlock) {
+    const int i = base + tid;
+    int64_t n = 0, all;
+    if (i < a.seqs) {
+      const Counts c = counts_of(a, i);
+      n = c.units;
+      if (c.bad && blockIdx.x == 0) atomicOr(a.p.err, kErrIndex);
+    }
+    if (base == 0) first = n;
+    const int64_t at = total + block_prefix<kBlock>(sc.warp_sum, n, &all);
+    if (blockIdx.x == 0 && i < a.seqs) ws.prefix[i] = at;
+    total += all;
+  }
+  if (blockIdx.x == 0 && tid == 0) ws.prefix[a.seqs] = total;
+  const int ctas = working(a, total), cta = static_cast<int>(blockIdx.x);
+  const int64_t u0 = cta < ctas ? first_unit(total, cta, ctas) : total;
+  const int64_t u1 = cta < ctas ? first_unit(total, cta + 1, ctas) : total;
+  if (tid == 0) {
+    sc.u0 = u0;
+    sc.u1 = u1;
+  }
+  // the sequence that holds u0
+  int64_t before = 0;
+  for (int base = 0; base < a.seqs && u0 < u1; base += kBlock) {
+    const int i = base + tid;
+    const int64_t n = i >= a.seqs ? 0 : base == 0 ? first : counts_of(a, i).units;
+    int64_t all;
+    const int64_t at = before + block_prefix<kBlock>(sc.warp_sum, n, &all);
+    if (n > 0 && u0 >= at && u0 < at + n) {
+      sc.seq = i;
+      sc.before = at;
+    }
+    before += all;
+    if (u0 < before) break;
+  }
+  __syncthreads();
+}
+
+// The segments of a run of units, one after the other.  Every role walks its
+// own copy.
+struct Walk {
+  int64_t u, end;     // units left: [u, end)
+  int64_t before;     // units before sequence `seq`
+  int seq;
+  Counts c;
+  __device__ __forceinline__ void start(const TreeArgs &a, const Scan &sc) {
+    u = sc.u0;
+    end = sc.u1;
+    seq = sc.seq;
+    before = sc.before;
+    if (u < end) c = counts_of(a, seq);
+  }
+  __device__ __forceinline__ bool next(const TreeArgs &a, Seg *s) {
+    if (u >= end) return false;
+    while (u >= before + c.units) {
+      before += c.units;
+      c = counts_of(a, ++seq);
+    }
+    const int64_t w = u - before, item = w / c.tiles;
+    s->t0 = static_cast<int>(w - item * c.tiles);
+    const int64_t left = end - u;
+    s->n = c.tiles - s->t0 < left ? c.tiles - s->t0 : static_cast<int>(left);
+    s->n0 = s->n;
+    s->head = static_cast<int>(item / c.row_tiles);
+    s->row0 = static_cast<int>(item - static_cast<int64_t>(s->head) * c.row_tiles) * a.item_rows;
+    const int rows = c.nodes * a.group - s->row0;
+    s->rows = rows < a.item_rows ? rows : a.item_rows;
+    s->two = s->rows > kBM;
+    s->keys = c.len;
+    s->q_base = c.q_base;
+    s->k_base = static_cast<int64_t>(seq) * a.max_pages;
+    s->nodes = c.nodes;
+    s->seq = seq;
+    s->diff = 0;
+    s->whole = s->n == c.tiles;
+    u += s->n;
+    return true;
+  }
+};
+
+// Node j's path to its root as bits.
+__device__ __forceinline__ uint64_t path_of(const TreeArgs &a, int64_t q_base, int j) {
+  if (!a.parents) return (2ull << j) - 1;
+  uint64_t path = 0;
+  for (int n = j; n >= 0;) {
+    path |= 1ull << n;
+    const int up = __ldg(a.parents + q_base + n);
+    n = up >= 0 && up < n ? up : -1;
+  }
+  return path;
+}
+
+// The 128-column mask of a row for the tile at key `pos`: all keys below
+// `base`, and node i's key base + i where bit i of `path` is set.
+__device__ __forceinline__ void tree_mask(int32_t pos, int32_t base, uint64_t path, uint32_t (&see)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int32_t off = base - (pos + 32 * g);  // columns below off come before the nodes
+    if (off >= 32) see[g] = 0xffffffffu;
+    else if (off >= 0) see[g] = ((1u << off) - 1u) | static_cast<uint32_t>(path << off);
+    else see[g] = off > -64 ? static_cast<uint32_t>(path >> -off) : 0u;
+  }
+}
+
+// The page of the row at token `pos`; a page out of range is reported and
+// page 0 read in its place.
+__device__ __forceinline__ int32_t page_at(const TreeArgs &a, int64_t table, int32_t pos) {
+  const int32_t page = __ldg(a.page_table + table + (pos >> a.p.page_shift));
+  if (page < 0 || page >= a.p.pages) {
+    atomicOr(a.p.err, kErrIndex);
+    return 0;
+  }
+  return page;
+}
+
+}  // namespace
+}  // namespace serve
+}  // namespace h3kv
