@@ -118,10 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (warp_on) {
         const int64_t n = see_keys - static_cast<int64_t>(t) * kBN;
-        const bool masked = __any_sync(0xffffffffu, n < kBN);
         uint32_t see[4];
-        prefix_mask(n, see);
-        softmax_tile<false>(tS, tO, t == t_first, masked, see, c2, row);
+        if (__any_sync(0xffffffffu, n < kBN)) {
+          prefix_mask(n, see);
+          softmax_tile<false, true>(tS, tO, t == t_first, see, c2, row);
+        } else {
+          softmax_tile<false, false>(tS, tO, t == t_first, see, c2, row);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -131,12 +134,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (s.n > 0) ok = ok && warp_wait(smem_u32(&sm.o_full), 0, w);
     tc_fence_after();
     // stream 1's maxima and sums for the join; both warpgroups leave together
-    if (!s.two && q == 1) sm.ml[i] = make_float2(row.m, row.l);
+    if (!s.two && q == 1) join_ml(sm)[i] = make_float2(row.m, row.l);
     ok = named_bar_and(1, 256, ok);
     if (ok && (s.two || q == 0)) {
       const bool joined = !s.two && s.n > 1;
       float ga = 1.f, gb = 0.f;
-      if (joined) join_rows(row, sm.ml[i], c2, ga, gb);
+      if (joined) join_rows(row, join_ml(sm)[i], c2, ga, gb);
       const float inv = row.l == 0.f ? 0.f : 1.f / row.l;
       if (warp_on) {
         // the row as bf16 into the Q tile (free now), 16-byte granule g of

@@ -14,39 +14,24 @@
 // takes 16 keys of a 128-key tile with a softmax of its own; the warps' results
 // are joined at the segment's end.
 //
-// Groups of 8 such warps take a tile each: two groups for 8 rows, one for 16
-// (whose registers would not leave room for two).  A producer warp copies whole
-// pages: codes by TMA with the 128-byte swizzle (so that the reads below spread
-// over the banks), scales by bulk copies, kStages tiles of 33 KB in flight.
+// 8 such warps; producer warps copy whole pages: codes by TMA with the 128-byte
+// swizzle (so that the reads below spread over the banks), scales by bulk
+// copies, kStages tiles of 33 KB in flight.  A step's codes are taken into
+// registers at once, so that a stage is empty while its products run.
 #include "tree.cuh"
 
 namespace h3kv {
 namespace serve {
 namespace {
 
-// Consumer warps, and the registers of a thread (setmaxnreg; 0: as launched).
-// 8 rows: 640 threads are launched with 96 registers each, 61440 in all; the
-// producer's warpgroup gives 72 of its 96 up, which lifts 512 threads to 112.
-template <int kNT>
-struct Shape;
-template <>
-struct Shape<1> {
-  static constexpr int kWarps = 16, kStages = 4;
-  static constexpr uint32_t kRegs = 112, kRegsProducer = 24;
-};
-template <>
-struct Shape<2> {
-  static constexpr int kWarps = 8, kStages = 5;
-  static constexpr uint32_t kRegs = 0, kRegsProducer = 0;
-};
-static_assert(16 * 32 * 112 + 4 * 32 * 24 <= 20 * 32 * 96, "register split");
-
+// Consumer warps and ring stages.
+constexpr int kWarps = 8, kProducers = 3, kStages = 5;
+constexpr int kFewThreads = (kWarps + kProducers + 1) * 32;
 constexpr int kCodeBytes = kBN * 128;      // one tile's codes
 constexpr int kPitch = 132;                // floats of a row in the join buffer
 
 template <int kNT>
 struct FewSmem {
-  static constexpr int kStages = Shape<kNT>::kStages, kWarps = Shape<kNT>::kWarps;
   uint8_t k[kStages][kCodeBytes];
   uint8_t v[kStages][kCodeBytes];
   float o[kWarps][8][kPitch];              // the warps' O, 8 rows at a time
@@ -56,9 +41,8 @@ struct FewSmem {
   uint64_t path[8 * kNT];
   uint64_t full[kStages], empty[kStages];
   Scan scan;
-  Walk walk;  // the consumers' (in shared memory: its 25 registers would spill)
-  Seg seg;
-  int more, abort;
+  SegRing segs;
+  int abort;
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -86,11 +70,10 @@ __device__ __forceinline__ uint32_t scale2(uint32_t x, uint32_t s) {
 }
 
 template <int kNT>
-__global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
+__global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   using S = FewSmem<kNT>;
-  constexpr int kStages = S::kStages, kWarps = S::kWarps, kGroups = kWarps / 8;
   S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Workspace ws = workspace_of(a);
@@ -99,52 +82,68 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
   if (tid == 0) pdl_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.full[s]), kProducers);
       mbar_init(smem_u32(&sm.empty[s]), 8);
     }
+    init_seg_ring(sm.segs, kWarps + kProducers);
     sm.abort = 0;
     fence_mbar_init();
   }
-  find_run<(kWarps + 4) * 32>(a, ws, sm.scan);
+  find_run<kFewThreads>(a, ws, sm.scan);
   if (sm.scan.u0 >= sm.scan.u1) return;
   const WaitCtx w{a.p.err, &sm.abort, a.timeout_ns};
 
+  SegReader sr;
+
+  if (warp == kWarps + kProducers) {
+    publish_segments(a, sm.scan, sm.segs, w);
+    return;
+  }
   if (warp >= kWarps) {
-    // ============================================================ producer
-    if constexpr (Shape<kNT>::kRegsProducer > 0) reg_dealloc<Shape<kNT>::kRegsProducer>();
-    if (warp > kWarps) return;
-    // lanes 0-7: K codes of the tile's pages, 8-15: V codes, 16-23 and 24-31:
-    // their scales
-    const int ps = a.p.page_size, piece = lane & 7, kind = lane >> 3;
-    const int at = piece * ps;
-    Walk walk;
-    Seg s;
-    walk.start(a, sm.scan);
+    // =========================================================== producers
+    // one warp each for K's codes, V's codes and the scales (one warp for all
+    // of them was what bounded the kernel); lanes 0-7 take the pages of a
+    // tile, lanes 8-15 V's scales
+    const int kind = warp - kWarps, ps = a.p.page_size;
+    const int at = (lane & 7) * ps;  // the lane's first row in the tile
+    const bool lane_on = lane < (kind == 2 ? 16 : 8) && at < kBN;
+    const CUtensorMap *map = kind == 0 ? &tm_k : &tm_v;
+    const uint32_t base = smem_u32(kind == 0 ? sm.k[0] : kind == 1 ? sm.v[0]
+                                   : reinterpret_cast<uint8_t *>(lane < 8 ? sm.ks[0] : sm.vs[0]));
+    const uint16_t *scales = lane < 8 ? a.p.k_scales : a.p.v_scales;
+    const uint32_t row_bytes = kind < 2 ? 128 : 2, tile_row_bytes = kind < 2 ? 128 : 4;
     int issued[kStages] = {};
     Ring<kStages> r;
     bool ok = true;
-    if (lane == 0) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-    }
-    while (ok && walk.next(a, &s)) {
-      for (int t = 0; t < s.n; ++t) {
-        const int32_t pos = (s.t0 + t) * kBN;
-        const int64_t left = s.keys - pos;
-        const int valid = left < kBN ? static_cast<int>(left) : kBN;
-        const bool on = at < valid;
-        int32_t row = 0;  // the page's first row in [pages, kv_heads, page_size]
-        if (on) row = (page_at(a, s.k_base, pos + at) * a.p.kv_heads + s.head) << a.p.page_shift;
+    if (lane == 0 && kind < 2) prefetch_tmap(map);
+    while (ok && (ok = sr.get(sm.segs, w))) {
+      const Seg &s = sr.seg(sm.segs);
+      const int n = s.n, t0 = s.t0, head = s.head;
+      const int64_t table = s.k_base;
+      const int32_t keys = static_cast<int32_t>(s.keys);
+      sr.done(sm.segs);
+      if (n == 0) break;
+      // the page of this lane in a tile, read one tile ahead
+      auto page_of = [&](int t) {
+        const int32_t p0 = (t0 + t) * kBN + at;
+        return lane_on && t < n && p0 < keys ? page_at(a, table, p0) : 0;
+      };
+      int32_t page = page_of(0);
+      for (int t = 0; t < n; ++t) {
+        const int32_t left = keys - (t0 + t) * kBN;
+        const int valid = left < kBN ? left : kBN;
+        // the page's first row in [pages, kv_heads, page_size]
+        const int32_t row = (page * a.p.kv_heads + head) << a.p.page_shift;
+        page = page_of(t + 1);
         if (!(ok = warp_wait(smem_u32(&sm.empty[r.slot]), r.phase ^ 1u, w))) break;
         const uint32_t bar = smem_u32(&sm.full[r.slot]);
-        const int pages = (valid + ps - 1) >> a.p.page_shift;
-        if (lane == 0) mbar_arrive_expect_tx(bar, 2 * pages * ps * 130);
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, (((valid + ps - 1) >> a.p.page_shift) << a.p.page_shift) * tile_row_bytes);
         __syncwarp();
-        if (on) {
-          if (kind == 0) tma_load_2d(smem_u32(sm.k[r.slot]) + at * 128, &tm_k, 0, row, bar);
-          else if (kind == 1) tma_load_2d(smem_u32(sm.v[r.slot]) + at * 128, &tm_v, 0, row, bar);
-          else if (kind == 2) bulk_g2s(smem_u32(sm.ks[r.slot]) + at * 2, a.p.k_scales + row, ps * 2, bar);
-          else bulk_g2s(smem_u32(sm.vs[r.slot]) + at * 2, a.p.v_scales + row, ps * 2, bar);
+        if (lane_on && at < valid) {
+          const uint32_t dst = base + (r.slot * kBN + at) * row_bytes;
+          if (kind < 2) tma_load_2d(dst, map, 0, row, bar);
+          else bulk_g2s(dst, scales + row, ps * 2, bar);
         }
         ++issued[r.slot];
         r.next();
@@ -159,28 +158,22 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
   }
 
   // ============================================================= consumers
-  if constexpr (Shape<kNT>::kRegs > 0) reg_alloc<Shape<kNT>::kRegs>();
   const int g8 = lane >> 2, i4 = lane & 3;   // MMA: row group and column pair
-  const int grp = warp >> 3;                 // takes tiles of its parity in the run
-  const int key0 = (warp & 7) * 16;          // its keys in a tile
+  const int key0 = warp * 16;          // its keys in a tile
   const float c2 = a.scale_log2;
   // its rows of the codes: the swizzle XORs the 16-byte chunk with row mod 8
   const uint32_t k_row = (key0 + g8) * 128, k_x = g8 & 7;
   const uint32_t v_row = (key0 + 2 * i4) * 128;
   Ring<kStages> r;
-  int tile = 0;  // of the run
-  const Seg &s = sm.seg;
-  if (tid == 0) sm.walk.start(a, sm.scan);
   for (;;) {
-    if (tid == 0) sm.more = sm.walk.next(a, &sm.seg);
-    named_bar_sync(1, kWarps * 32);
-    if (!sm.more) break;
+    bool ok = sr.get(sm.segs, w);
+    const Seg &s = sr.seg(sm.segs);
     // q' = fp16(q H) of the segment's rows, rows behind them 0
-    if (warp < 2 * kNT) {
+    if (ok && s.n > 0 && warp < 2 * kNT) {
       const int row = warp * 4 + (lane >> 3), l = lane & 7;
       uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
       if (row < s.rows) {
-        const int x = s.row0 + row, node = x / a.group, h = s.head * a.group + (x - node * a.group);
+        const int x = s.row0 + row, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
         const uint4 *src =
             reinterpret_cast<const uint4 *>(a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride) + l;
         raw[0] = __ldg(src);
@@ -201,7 +194,9 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
       dst[8] = make_uint4(pack_f16x2(v[8], v[9]), pack_f16x2(v[10], v[11]), pack_f16x2(v[12], v[13]),
                           pack_f16x2(v[14], v[15]));
     }
-    named_bar_sync(1, kWarps * 32);
+    // the warps go on, or leave, together
+    ok = named_bar_and(1, kWarps * 32, ok);
+    if (!ok || s.n == 0) break;
     // B fragments of q'^T: of row g8 the 16 channels of chunk i4 (and i4 + 4),
     // four of them for each k step: the channel order that K's chunks give
     uint32_t qf[kNT][16];
@@ -225,52 +220,71 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
       m[nt][0] = m[nt][1] = kNoMax;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    bool ok = true;
     const int32_t keys = static_cast<int32_t>(s.keys);
     const int n_tiles = s.n;
     int32_t pos = s.t0 * kBN + key0;
-    for (int t = 0; t < n_tiles; ++t, ++tile, pos += kBN) {
-      if (tile % kGroups != grp) {
-        r.next();
-        continue;
-      }
+    for (int t = 0; t < n_tiles; ++t, pos += kBN) {
       if (!warp_wait(smem_u32(&sm.full[r.slot]), r.phase, w)) {
         ok = false;
         break;
       }
-      if (pos < keys) {
-        const uint8_t *kb = sm.k[r.slot], *vb = sm.v[r.slot];
-        // S^T: keys g8 and g8 + 8, rows 2 i4 + {0, 1}
-        float st[kNT][4];
-        const uint32_t k0 = sm.ks[r.slot][key0 + g8] * 0x10001u, k1 = sm.ks[r.slot][key0 + g8 + 8] * 0x10001u;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) st[nt][0] = st[nt][1] = st[nt][2] = st[nt][3] = 0.f;
+      // the step's codes and scales into registers, and the stage is free again
+      uint4 kw[2][2], vw[4];
+      uint32_t k0, k1, v0, v1;
+      {
+        const uint8_t *kb = sm.k[r.slot] + k_row, *vb = sm.v[r.slot] + v_row;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint32_t c = ((i4 + 4 * hf) ^ k_x) << 4;
-          const uint4 x = *reinterpret_cast<const uint4 *>(kb + k_row + c);
-          const uint4 y = *reinterpret_cast<const uint4 *>(kb + k_row + 8 * 128 + c);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+          kw[hf][0] = *reinterpret_cast<const uint4 *>(kb + c);
+          kw[hf][1] = *reinterpret_cast<const uint4 *>(kb + 8 * 128 + c);
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t ux = xw[j] ^ 0x80808080u, uy = yw[j] ^ 0x80808080u;
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t row = 2 * i4 + (x & 1);  // mod 8 (keys 8 later: the same)
+          vw[x] = *reinterpret_cast<const uint4 *>(vb + ((x & 1) + 8 * (x >> 1)) * 128 + ((g8 ^ row) << 4));
+        }
+        k0 = sm.ks[r.slot][key0 + g8] * 0x10001u;
+        k1 = sm.ks[r.slot][key0 + g8 + 8] * 0x10001u;
+        v0 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4]);
+        v1 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4 + 8]);
+      }
+      __syncwarp();
+      // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
+      if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.empty[r.slot]));
+      r.next();
+      if (pos < keys) {
+        // S^T: keys g8 and g8 + 8, rows 2 i4 + {0, 1}; the channels in two
+        // sums, so that the MMAs wait less for one another
+        float st[kNT][4], su[kNT][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          st[nt][0] = st[nt][1] = st[nt][2] = st[nt][3] = 0.f;
+          su[nt][0] = su[nt][1] = su[nt][2] = su[nt][3] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint4 x = kw[hf][0], y = kw[hf][1];
+            const uint32_t ux = (j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w) ^ 0x80808080u;
+            const uint32_t uy = (j == 0 ? y.x : j == 1 ? y.y : j == 2 ? y.z : y.w) ^ 0x80808080u;
             const uint32_t af[4] = {scale2(unbias(__byte_perm(ux, 0x64646464u, 0x4140)), k0),
                                     scale2(unbias(__byte_perm(uy, 0x64646464u, 0x4140)), k1),
                                     scale2(unbias(__byte_perm(ux, 0x64646464u, 0x4342)), k0),
                                     scale2(unbias(__byte_perm(uy, 0x64646464u, 0x4342)), k1)};
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mma16816(st[nt], af, qf[nt][8 * hf + 2 * j], qf[nt][8 * hf + 2 * j + 1]);
+            for (int nt = 0; nt < kNT; ++nt)
+              mma16816(hf ? su[nt] : st[nt], af, qf[nt][8 * hf + 2 * j], qf[nt][8 * hf + 2 * j + 1]);
           }
         }
         // scores in log2 units; keys behind the sequence and nodes off the
         // row's path do not count
-        uint32_t v0 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4]);
-        uint32_t v1 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4 + 8]);
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st[nt][e] *= c2;
+          for (int e = 0; e < 4; ++e) st[nt][e] = (st[nt][e] + su[nt][e]) * c2;
         }
         if (pos + 16 > base_key) {
           const int32_t n0 = pos + g8 - base_key, n1 = n0 + 8;
@@ -328,13 +342,6 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
         }
         // O^T: channels 16 g8 + 2 t (+ 1) in m tile t; V'^T's pairs run along
         // the keys 2 i4 + {0, 1} (+ 8)
-        uint4 vw[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t row = 2 * i4 + (x & 1);  // mod 8 (keys 8 later: the same)
-          vw[x] = *reinterpret_cast<const uint4 *>(vb + v_row + ((x & 1) + 8 * (x >> 1)) * 128 +
-                                                   ((g8 ^ (row & 7)) << 4));
-        }
         const uint32_t wd[4][4] = {{vw[0].x, vw[0].y, vw[0].z, vw[0].w},
                                    {vw[1].x, vw[1].y, vw[1].z, vw[1].w},
                                    {vw[2].x, vw[2].y, vw[2].z, vw[2].w},
@@ -355,10 +362,6 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
           }
         }
       }
-      __syncwarp();
-      // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
-      if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.empty[r.slot]));
-      r.next();
     }
     // join the warps: common maximum, then the sum of the rescaled parts in order
 #pragma unroll
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
       }
       named_bar_sync(1, kWarps * 32);
       const int row = 8 * nt + warp;
-      if (warp < 8 && row < s.rows) {
+      if (row < s.rows) {
         float top = sm.m[0][row], sum = 0.f;
 #pragma unroll
         for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm.m[x][row]);
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
           v[3] += y.w;
         }
         if (s.whole) {
-          const int x = s.row0 + row, node = x / a.group, h = s.head * a.group + (x - node * a.group);
+          const int x = s.row0 + row, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
           fwht128_warp(v, lane);
           const float inv = kInvSqrt128 / sum;
           *reinterpret_cast<uint2 *>(a.o.data + h * a.o.head_stride + (s.q_base + node) * a.o.row_stride + 4 * lane) =
@@ -423,6 +426,7 @@ __global__ void __launch_bounds__((Shape<kNT>::kWarps + 4) * 32, 1)
       }
       named_bar_sync(1, kWarps * 32);
     }
+    sr.done(sm.segs);
   }
 }
 
@@ -432,7 +436,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs 
   static_assert(kBytes <= 232448, "shared memory budget");
   const cudaError_t e = cudaFuncSetAttribute(few_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  few_kernel<kNT><<<a.ctas, (Shape<kNT>::kWarps + 4) * 32, kBytes, stream>>>(tk, tv, a);
+  few_kernel<kNT><<<a.ctas, kFewThreads, kBytes, stream>>>(tk, tv, a);
   return cudaGetLastError();
 }
 

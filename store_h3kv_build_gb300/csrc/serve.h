@@ -51,10 +51,12 @@ struct TreeArgs {
   const int32_t *page_table, *lengths, *cu_nodes, *parents;
   int64_t max_pages, nodes;
   int32_t q_heads, group, seqs;
+  uint32_t group_magic;  // ceil(2^19 / group)
   float scale_log2;
   float *workspace;
   int32_t ctas;
-  int32_t item_rows;   // rows of a row tile, by the kernel that runs
+  int32_t item_rows;   // rows of a row tile, by the kernel that runs, and
+  int32_t item_cost;   //   what one costs beside its key tiles, in tiles
   uint64_t timeout_ns;
   int32_t withhold_p_tile1;
 };

@@ -55,7 +55,6 @@ struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kNK][kTileBytes];
   uint8_t v[kNV][kTileBytes];
-  float2 ml[kBM];  // stream 1's (max, sum) for the join with stream 0
   uint64_t q_full[2];
   uint64_t k_load[kNK], k_ready[kNK], k_free[kNK];
   uint64_t v_load[kNV], v_ready[kNV], v_free[kNV];
@@ -68,6 +67,10 @@ struct Smem {
   uint32_t tmem_base;
   int abort;
 };
+// Stream 1's (max, sum) for the join with stream 0 lie in its Q tile, which is
+// free once the segment's products are done.
+__device__ __forceinline__ float2 *join_ml(Smem &sm) { return reinterpret_cast<float2 *>(sm.q[1]); }
+
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -260,15 +263,18 @@ struct Row {
 };
 
 // One 128-key tile: S from TMEM, mask, running maximum, P back to TMEM.
-// `masked` (warp-uniform): only the columns set in `see` count.
-template <bool kF16>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, bool masked,
-                                             const uint32_t (&see)[4], float c2, Row &r) {
+// kMasked: only the columns set in `see` count.
+template <bool kF16, bool kMasked>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, const uint32_t (&see)[4], float c2,
+                                             Row &r) {
   float s[128];
-  float m4[4];
-  tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
-  float mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-  if (masked) {
+  float mt;
+  if constexpr (!kMasked) {
+    float m4[4];
+    tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
+    mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+  } else {
+    tmem_ld128(tS, *reinterpret_cast<uint32_t(*)[128]>(s));
 #pragma unroll
     for (int c = 0; c < 128; ++c) s[c] = (see[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
     float m8[8];
