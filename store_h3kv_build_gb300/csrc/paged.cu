@@ -4,134 +4,267 @@
 // All four are bound by HBM at size and by latency for a decoding step's few
 // rows; none has arithmetic worth a tensor core.
 #include "ptx.cuh"
+#include "attend.cuh"
 #include "serve_rows.cuh"
+#include "store_fwht.cuh"
 
 namespace h3kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerCta = kThreads / 8;
 
 // Pool row `r` -> its row in [pages, kv_heads, page_size].
 __device__ __forceinline__ int64_t pool_row(const PagedArgs &p, int32_t r, int32_t head) {
   return ((static_cast<int64_t>(r >> p.page_shift) * p.kv_heads + head) << p.page_shift) + (r & (p.page_size - 1));
 }
+// Pool row of token `t`, -1 if it is left out (or out of range, which is
+// reported).
+__device__ __forceinline__ int32_t row_of_token(const PagedArgs &p, const int32_t *__restrict__ rows, int64_t t,
+                                                int64_t n) {
+  const int32_t r = t < n ? __ldg(rows + t) : -1;
+  if (r < p.pages * p.page_size) return r;
+  atomicOr(p.err, kErrIndex);
+  return -1;
+}
 
-// What a CTA works on: 32 tokens of one head of K or of V.
-struct Piece {
-  int64_t token;
-  int32_t head;
-  bool v;
+// ----------------------------------------------------------------- append --
+// A persistent CTA walks 128-token tiles of one head of K or of V; a producer
+// warp streams them into a ring with TMA (whatever the strides), and two
+// threads share a row.  H128 = [[H64, H64], [H64, -H64]]: thread hf forms the
+// sum (hf 0) or difference (hf 1) of the row's halves and transforms 64 values
+// in registers, so a row costs no shuffle but the one for its absmax.  (With a
+// row over 8 lanes, 48 shuffles for 4 rows, it ran at 3.5 TB/s.)
+constexpr int kTokens = 128;
+constexpr int kComputeWarps = 2 * kTokens / 32;
+constexpr int kAppendThreads = 2 * kTokens + 32;
+constexpr int kAppendStages = 3;
+constexpr int kTokenTileBytes = kTokens * 256;
+
+struct AppendSmem {
+  uint8_t in[kAppendStages][kTokenTileBytes];
+  uint64_t full[kAppendStages], empty[kAppendStages];
+  int abort;
 };
-__device__ __forceinline__ Piece piece_of(int64_t n, int32_t kv_heads) {
-  const uint32_t groups = static_cast<uint32_t>((n + kRowsPerCta - 1) / kRowsPerCta);
-  const uint32_t b = blockIdx.x, y = b / groups;
-  return {static_cast<int64_t>(b - y * groups) * kRowsPerCta + (threadIdx.x >> 3), static_cast<int32_t>(y >> 1),
-          (y & 1) != 0};
-}
+constexpr int kAppendSmemBytes = sizeof(AppendSmem) + 1024;
 
+// Four codes rne(x m), clamped to [-127, 127], packed (the conversion packs
+// and saturates from above; -128 is kept out before).
 __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float m) {
-  auto q = [m](float x) {
-    const int v = __float2int_rn(x * m);
-    return static_cast<uint32_t>(v > 127 ? 127 : v < -127 ? -127 : v) & 0xFFu;
-  };
-  return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
+  const int ia = __float2int_rn(fmaxf(a * m, -127.f)), ib = __float2int_rn(fmaxf(b * m, -127.f));
+  const int ic = __float2int_rn(fmaxf(c * m, -127.f)), id = __float2int_rn(fmaxf(d * m, -127.f));
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\t"
+      "cvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\t"
+      "cvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+      : "=r"(r)
+      : "r"(ia), "r"(ib), "r"(ic), "r"(id));
+  return r;
 }
 
-// A warp takes 4 rows, 8 lanes each: 32 bytes of a row per thread, one
-// 16-bit scale per row, 16 code bytes per thread.
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(const PagedArgs p, const h3kv_rows K, const h3kv_rows V, const int32_t *__restrict__ rows,
-                  const int64_t n) {
-  const Piece w = piece_of(n, p.kv_heads);
-  const int l = threadIdx.x & 7;
-  int32_t r = -1;
-  if (w.token < n) r = __ldg(rows + w.token);
-  if (r >= p.pages * p.page_size) {
-    if (l == 0) atomicOr(p.err, kErrIndex);
-    r = -1;
+template <bool kWide>
+__global__ void __launch_bounds__(kAppendThreads, 2)
+    append_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const PagedArgs p, const int32_t *__restrict__ rows, const int64_t n, const uint64_t timeout_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  AppendSmem &sm = *reinterpret_cast<AppendSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t token_tiles = (n + kTokens - 1) / kTokens, tiles = token_tiles * p.kv_heads * 2;
+  if (tid == 0) {
+    for (int s = 0; s < kAppendStages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), kComputeWarps);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
   }
-  const h3kv_rows &in = w.v ? V : K;
-  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-  if (r >= 0) {
-    const uint4 *src =
-        reinterpret_cast<const uint4 *>(in.data + w.head * in.head_stride + w.token * in.row_stride) + l;
-    lo = __ldcs(src);
-    hi = __ldcs(src + 8);
+  __syncthreads();
+  const WaitCtx w{p.err, &sm.abort, timeout_ns};
+  int slot = 0;
+  uint32_t phase = 0;
+  if (warp == kComputeWarps) {
+    const uint32_t go = elect_one();
+    int issued[kAppendStages] = {};
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int64_t y = t / token_tiles;
+      const int32_t token = static_cast<int32_t>(t - y * token_tiles) * kTokens, head = static_cast<int32_t>(y >> 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.empty[slot]), phase ^ 1u, w))) break;
+      if (go) {
+        const CUtensorMap *map = (y & 1) ? &tm_v : &tm_k;
+        const uint32_t bar = smem_u32(&sm.full[slot]), dst = smem_u32(sm.in[slot]);
+        mbar_arrive_expect_tx(bar, kTokenTileBytes);
+        tma_load_3d(dst, map, 0, token, head, bar);
+        tma_load_3d(dst + kTokenTileBytes / 2, map, 64, token, head, bar);
+      }
+      ++issued[slot];
+      if (++slot == kAppendStages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    if (sm.abort) {
+      // every copy that was issued must land before the CTA exits
+      for (int s = 0; s < kAppendStages; ++s)
+        if (issued[s]) mbar_wait_drain(smem_u32(&sm.full[s]), (issued[s] - 1) & 1, kDrainNs);
+    }
+    return;
   }
-  float x[16];
-  unpack_bf16x8(lo, x);
-  unpack_bf16x8(hi, x + 8);
-  // 2^-7 first (exact), so that a sum of 128 of the largest bf16 values stays
-  // finite; the values that it makes subnormal lie far below the least scale
+  const int i = tid >> 1, hf = tid & 1;  // row in the tile, half of the result
+  const float2 sign = hf ? make_float2(-1.f, -1.f) : make_float2(1.f, 1.f);
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t y = t / token_tiles, token = (t - y * token_tiles) * kTokens + i;
+    const int32_t head = static_cast<int32_t>(y >> 1);
+    const int32_t r = row_of_token(p, rows, token, n);
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), phase, w))) return;
+    // 2^-7 first (exact), so that a sum of 128 of the largest bf16 values stays
+    // finite; the values that it makes subnormal lie far below the least scale
+    float x[64];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] *= 0.0078125f;
-  fwht128_oct(x, l);
-  float a = 0.f;
+    for (int g = 0; g < 8; ++g) {
+      const uint32_t off = sw128_off(i, g);
+      float lo[8], hi[8];
+      unpack_bf16x8(*reinterpret_cast<const uint4 *>(sm.in[slot] + off), lo);
+      unpack_bf16x8(*reinterpret_cast<const uint4 *>(sm.in[slot] + kTokenTileBytes / 2 + off), hi);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]));
+      for (int e = 0; e < 8; e += 2) {
+        const float2 k = make_float2(0.0078125f, 0.0078125f);
+        const float2 a = __fmul2_rn(make_float2(lo[e], lo[e + 1]), k);
+        const float2 b = __fmul2_rn(make_float2(hi[e], hi[e + 1]), k);
+        const float2 s = __ffma2_rn(b, sign, a);
+        x[8 * g + e] = s.x;
+        x[8 * g + e + 1] = s.y;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+    if (++slot == kAppendStages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    fwht64_packed(x);
+    float a = 0.f;
 #pragma unroll
-  for (int m = 1; m < 8; m <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
-  // s = fp16(absmax(x H) / 127), saturated; codes rne(x H / s) with the stored s.
-  // absmax * sqrt(128) / 127 in two fp32 parts p + e: where p alone lies on
-  // the tie between two fp16 values, e says which side the product is on.
-  constexpr float kHi = 0.08908431977033615f, kLo = -8.806923523785315e-10f;  // sqrt(128) / 127
-  float scale = a * kHi;
-  const float e = fmaf(a, kLo, fmaf(a, kHi, -scale));
-  uint32_t bits = __float_as_uint(scale);
-  if ((bits & 0x1FFFu) == 0x1000u) scale = __uint_as_float(bits + (e > 0.f ? 1 : e < 0.f ? -1 : 0));
-  __half s = __float2half_rn(scale);
-  if (__hisinf(s)) s = __ushort_as_half(0x7BFFu);
-  const float sf = __half2float(s);
-  const float m = sf > 0.f ? kInvSqrt128 * 128.0f / sf : 0.f;
-  if (r >= 0) {
-    const int64_t at = pool_row(p, r, w.head);
-    uint2 *dst = reinterpret_cast<uint2 *>((w.v ? p.v_codes : p.k_codes) + at * 128) + l;
-    dst[0] = make_uint2(code4(x[0], x[1], x[2], x[3], m), code4(x[4], x[5], x[6], x[7], m));
-    dst[8] = make_uint2(code4(x[8], x[9], x[10], x[11], m), code4(x[12], x[13], x[14], x[15], m));
-    if (l == 0) (w.v ? p.v_scales : p.k_scales)[at] = __half_as_ushort(s);
+    for (int e = 0; e < 64; ++e) a = fmaxf(a, fabsf(x[e]));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    // s = fp16(absmax(x H) / 127), saturated; codes rne(x H / s) with the stored
+    // s.  absmax * sqrt(128) / 127 in two fp32 parts p + e: where p alone lies
+    // on the tie between two fp16 values, e says which side the product is on.
+    constexpr float kHi = 0.08908431977033615f, kLo = -8.806923523785315e-10f;  // sqrt(128) / 127
+    float scale = a * kHi;
+    const float e = fmaf(a, kLo, fmaf(a, kHi, -scale));
+    const uint32_t bits = __float_as_uint(scale);
+    if ((bits & 0x1FFFu) == 0x1000u) scale = __uint_as_float(bits + (e > 0.f ? 1 : e < 0.f ? -1 : 0));
+    __half s = __float2half_rn(scale);
+    if (__hisinf(s)) s = __ushort_as_half(0x7BFFu);
+    const float sf = __half2float(s);
+    const float m = sf > 0.f ? kInvSqrt128 * 128.0f / sf : 0.f;
+    if (r >= 0) {
+      const int64_t at = pool_row(p, r, head);
+      uint8_t *dst = reinterpret_cast<uint8_t *>((y & 1) ? p.v_codes : p.k_codes) + at * 128 + hf * 64;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int at4 = 32 * g + 4 * k;
+          c[k] = code4(x[at4], x[at4 + 1], x[at4 + 2], x[at4 + 3], m);
+        }
+        if constexpr (kWide) {
+          st_global_v8(dst + 32 * g, c);
+        } else {
+          reinterpret_cast<uint4 *>(dst)[2 * g] = make_uint4(c[0], c[1], c[2], c[3]);
+          reinterpret_cast<uint4 *>(dst)[2 * g + 1] = make_uint4(c[4], c[5], c[6], c[7]);
+        }
+      }
+      if (hf == 0) ((y & 1) ? p.v_scales : p.k_scales)[at] = __half_as_ushort(s);
+    }
   }
 }
 
-// The inverse: 16 code bytes per thread, dequantised as the attention does
-// (fp16(code * scale)), un-rotated in fp32 and rounded to bf16 once.
-__global__ void __launch_bounds__(kThreads)
+// ------------------------------------------------------------------- read --
+// Two threads share a row here too: each dequantises its 64 codes as the
+// attention does (fp16(code * scale)) and transforms them, then the pair
+// exchanges sums and differences (H128 = H2 x H64).  The next tile's codes, and
+// the row numbers of the one after it, are loaded before the present one is
+// worked on.
+template <bool kWide>
+__global__ void __launch_bounds__(kThreads, 2)
     read_kernel(const PagedArgs p, const int32_t *__restrict__ rows, const int64_t n, const h3kv_rows K,
                 const h3kv_rows V) {
-  const Piece w = piece_of(n, p.kv_heads);
-  const int l = threadIdx.x & 7;
-  int32_t r = -1;
-  if (w.token < n) r = __ldg(rows + w.token);
-  if (r >= p.pages * p.page_size) {
-    if (l == 0) atomicOr(p.err, kErrIndex);
-    r = -1;
-  }
-  uint2 c[2] = {make_uint2(0, 0), make_uint2(0, 0)};
-  __half s = __ushort_as_half(0);
-  if (r >= 0) {
-    const int64_t at = pool_row(p, r, w.head);
-    const uint2 *src = reinterpret_cast<const uint2 *>((w.v ? p.v_codes : p.k_codes) + at * 128) + l;
-    c[0] = src[0];
-    c[1] = src[8];
-    s = __ushort_as_half((w.v ? p.v_scales : p.k_scales)[at]);
-  }
-  float x[16];
+  const int i = threadIdx.x >> 1, hf = threadIdx.x & 1;
+  const int64_t token_tiles = (n + kTokens - 1) / kTokens, tiles = token_tiles * p.kv_heads * 2;
+  struct Row {
+    uint4 c[4];
+    uint16_t s;
+  };
+  auto index = [&](int64_t t) {
+    return t < tiles ? row_of_token(p, rows, t % token_tiles * kTokens + i, n) : -1;
+  };
+  auto load = [&](int64_t t, int32_t r) {
+    Row x;
+    x.s = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t word = (i & 4) ? c[i >> 3].y : c[i >> 3].x;
-    const int code = static_cast<int8_t>(word >> ((i & 3) * 8));
-    x[i] = __half2float(__hmul(__int2half_rn(code), s));
-  }
-  fwht128_oct(x, l);
-  if (w.token < n) {
-    const h3kv_rows &out = w.v ? V : K;
-    uint4 *dst = reinterpret_cast<uint4 *>(out.data + w.head * out.head_stride + w.token * out.row_stride) + l;
+    for (int g = 0; g < 4; ++g) x.c[g] = make_uint4(0, 0, 0, 0);
+    if (r >= 0) {
+      const int64_t y = t / token_tiles, at = pool_row(p, r, static_cast<int32_t>(y >> 1));
+      const uint4 *src = reinterpret_cast<const uint4 *>(((y & 1) ? p.v_codes : p.k_codes) + at * 128) + hf * 4;
+      if constexpr (kWide) {
+        ld_global_v8(src, x.c[0], x.c[1]);
+        ld_global_v8(src + 2, x.c[2], x.c[3]);
+      } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= kInvSqrt128;
-    dst[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                        pack_bf16x2(x[6], x[7]));
-    dst[8] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
-                        pack_bf16x2(x[14], x[15]));
+        for (int g = 0; g < 4; ++g) x.c[g] = src[g];
+      }
+      x.s = ((y & 1) ? p.v_scales : p.k_scales)[at];
+    }
+    return x;
+  };
+  Row next = load(blockIdx.x, index(blockIdx.x));
+  int32_t r = index(static_cast<int64_t>(blockIdx.x) + gridDim.x);
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const Row row = next;
+    next = load(t + gridDim.x, r);
+    r = index(t + 2 * static_cast<int64_t>(gridDim.x));
+    float x[64];
+    const __half s = __ushort_as_half(row.s);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t h[8];
+      attn::dequant16(row.c[g], __halves2half2(s, s), h);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+        x[16 * g + 2 * k] = f.x;
+        x[16 * g + 2 * k + 1] = f.y;
+      }
+    }
+    fwht64_packed(x);
+    const float2 norm = make_float2(kInvSqrt128, kInvSqrt128);
+    const float2 sign = hf ? make_float2(-1.f, -1.f) : make_float2(1.f, 1.f);
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) {
+      const float2 v = __fmul2_rn(make_float2(x[e], x[e + 1]), norm);
+      const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v.x, 1), __shfl_xor_sync(0xffffffffu, v.y, 1));
+      const float2 z = __ffma2_rn(v, sign, o);  // lo + hi, or lo - hi in the second half
+      x[e] = z.x;
+      x[e + 1] = z.y;
+    }
+    const int64_t y = t / token_tiles, token = (t - y * token_tiles) * kTokens + i;
+    if (token < n) {
+      const h3kv_rows &out = (y & 1) ? V : K;
+      uint4 *dst = reinterpret_cast<uint4 *>(out.data + (y >> 1) * out.head_stride + token * out.row_stride) + hf * 8;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = pack_bf16x2(x[16 * g + 2 * k], x[16 * g + 2 * k + 1]);
+        if constexpr (kWide) {
+          st_global_v8(dst + 2 * g, c);
+        } else {
+          dst[2 * g] = make_uint4(c[0], c[1], c[2], c[3]);
+          dst[2 * g + 1] = make_uint4(c[4], c[5], c[6], c[7]);
+        }
+      }
+    }
   }
 }
 
@@ -257,18 +390,34 @@ bool grid_of(int64_t a, int64_t b, int64_t c, unsigned *out) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedArgs &p, const h3kv_rows &K, const h3kv_rows &V, const int32_t *rows,
-                                int64_t n, cudaStream_t stream) {
-  unsigned grid;
-  if (!grid_of((n + kRowsPerCta - 1) / kRowsPerCta, p.kv_heads, 2, &grid)) return cudaErrorInvalidValue;
-  append_kernel<<<grid, kThreads, 0, stream>>>(p, K, V, rows, n);
+                                int64_t n, const ServeDevice &d, cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  if (!encode_rows_bf16(&tk, K, p.kv_heads, n, kTokens) || !encode_rows_bf16(&tv, V, p.kv_heads, n, kTokens))
+    return cudaErrorInvalidValue;
+  // whole 32-byte sectors per store where the codes' alignment allows
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.k_codes) | reinterpret_cast<uintptr_t>(p.v_codes)) & 31) == 0;
+  auto kernel = wide ? append_kernel<true> : append_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (n + kTokens - 1) / kTokens * p.kv_heads * 2;
+  const unsigned grid = static_cast<unsigned>(tiles < 2 * d.num_sms ? tiles : 2 * d.num_sms);
+  kernel<<<grid, kAppendThreads, kAppendSmemBytes, stream>>>(tk, tv, p, rows, n, d.timeout_ns);
   return cudaGetLastError();
 }
 
 cudaError_t launch_paged_read(const PagedArgs &p, const int32_t *rows, int64_t n, const h3kv_rows &K,
-                              const h3kv_rows &V, cudaStream_t stream) {
-  unsigned grid;
-  if (!grid_of((n + kRowsPerCta - 1) / kRowsPerCta, p.kv_heads, 2, &grid)) return cudaErrorInvalidValue;
-  read_kernel<<<grid, kThreads, 0, stream>>>(p, rows, n, K, V);
+                              const h3kv_rows &V, const ServeDevice &d, cudaStream_t stream) {
+  const int64_t tiles = (n + kTokens - 1) / kTokens * p.kv_heads * 2;
+  const unsigned grid = static_cast<unsigned>(tiles < 2 * d.num_sms ? tiles : 2 * d.num_sms);
+  // whole 32-byte sectors per load and store where the alignment allows
+  auto low_bits = [&](const h3kv_rows &r) {
+    return reinterpret_cast<uintptr_t>(r.data) | static_cast<uintptr_t>(r.head_stride * 2) |
+           static_cast<uintptr_t>(r.row_stride * 2);
+  };
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.k_codes) | reinterpret_cast<uintptr_t>(p.v_codes) | low_bits(K) |
+                      low_bits(V)) &
+                     31) == 0;
+  (wide ? read_kernel<true> : read_kernel<false>)<<<grid, kThreads, 0, stream>>>(p, rows, n, K, V);
   return cudaGetLastError();
 }
 

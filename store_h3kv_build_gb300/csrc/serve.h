@@ -35,9 +35,9 @@ struct PagedArgs {
 };
 
 cudaError_t launch_paged_append(const PagedArgs &p, const h3kv_rows &K, const h3kv_rows &V, const int32_t *rows,
-                                int64_t n, cudaStream_t stream);
+                                int64_t n, const ServeDevice &d, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedArgs &p, const int32_t *rows, int64_t n, const h3kv_rows &K,
-                              const h3kv_rows &V, cudaStream_t stream);
+                              const h3kv_rows &V, const ServeDevice &d, cudaStream_t stream);
 cudaError_t launch_paged_copy(const PagedArgs &p, const int32_t *src, const int32_t *dst, int64_t n,
                               cudaStream_t stream);
 cudaError_t launch_paged_keep(const PagedArgs &p, const int32_t *page_table, int64_t max_pages,

@@ -91,7 +91,7 @@ h3kv_status h3kv_paged_append(const h3kv_rows *K, const h3kv_rows *V, const int3
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   p.err = d.err;
-  return status_of(h3kv::launch_paged_append(p, *K, *V, rows, n, static_cast<cudaStream_t>(stream)));
+  return status_of(h3kv::launch_paged_append(p, *K, *V, rows, n, d, static_cast<cudaStream_t>(stream)));
 }
 
 h3kv_status h3kv_paged_read(const h3kv_paged_store *store, const int32_t *rows, int64_t n, const h3kv_rows *K,
@@ -106,7 +106,7 @@ h3kv_status h3kv_paged_read(const h3kv_paged_store *store, const int32_t *rows, 
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   p.err = d.err;
-  return status_of(h3kv::launch_paged_read(p, rows, n, *K, *V, static_cast<cudaStream_t>(stream)));
+  return status_of(h3kv::launch_paged_read(p, rows, n, *K, *V, d, static_cast<cudaStream_t>(stream)));
 }
 
 h3kv_status h3kv_paged_copy(const h3kv_paged_store *store, const int32_t *src, const int32_t *dst, int64_t n,

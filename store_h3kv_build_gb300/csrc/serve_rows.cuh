@@ -7,6 +7,13 @@
 
 namespace h3kv {
 
+// 32 bytes from global memory; the address must be 32-byte aligned.
+__device__ __forceinline__ void ld_global_v8(const void *p, uint4 &a, uint4 &b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
 __device__ __forceinline__ void unpack_bf16x8(const uint4 w, float *x) {
   x[0] = bf16lo_to_f32(w.x);
   x[1] = bf16hi_to_f32(w.x);
