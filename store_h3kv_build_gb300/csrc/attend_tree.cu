@@ -10,7 +10,7 @@ namespace {
 
 struct TreeSmem : Smem {
   Scan scan;
-  SegRing segs;
+  TreeSegs segs;
 };
 constexpr size_t kTreeSmemBytes = sizeof(TreeSmem) + 1024;
 static_assert(kTreeSmemBytes <= 232448, "shared memory budget");
@@ -27,7 +27,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, TreeSmem &sm, uint8_t
   const int at = lane * ps;  // the lane's first row in the tile
   int issued[kDepth] = {};
   Ring<kDepth> r;
-  SegReader sr;
+  TreeReader sr;
   bool ok = true;
   while (ok && (ok = sr.get(sm.segs, w))) {
     const Seg &s = sr.seg(sm.segs);
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const WaitCtx w{a.p.err, &sm.abort, a.timeout_ns};
-  SegReader sr;
+  TreeReader sr;
 
   if (warp < 8) {
     // =================================================== softmax warpgroups

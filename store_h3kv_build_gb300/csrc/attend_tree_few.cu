@@ -41,7 +41,7 @@ struct FewSmem {
   uint64_t path[8 * kNT];
   uint64_t full[kStages], empty[kStages];
   Scan scan;
-  SegRing segs;
+  TreeSegs segs;
   int abort;
 };
 
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (sm.scan.u0 >= sm.scan.u1) return;
   const WaitCtx w{a.p.err, &sm.abort, a.timeout_ns};
 
-  SegReader sr;
+  TreeReader sr;
 
   if (warp == kWarps + kProducers) {
     publish_segments(a, sm.scan, sm.segs, w);

@@ -60,10 +60,8 @@ struct Smem {
   uint64_t v_load[kNV], v_ready[kNV], v_free[kNV];
   uint64_t s_full[2], p_full[2];
   uint64_t o_full, drain;
-  uint64_t v_tail, v_fixed;  // prompts: a ragged last V tile copied; its rest zeroed
-  int64_t scan_prefix, scan_total;
-  int64_t warp_sum[16];
-  int scan_seq;
+  uint64_t q_free[2];        // prompts: the stream's last QK of a segment is done
+  uint64_t v_tail, v_fixed;  // prompts: a ragged last V tile has come; its rest is zeroed
   uint32_t tmem_base;
   int abort;
 };
@@ -111,10 +109,42 @@ __device__ __forceinline__ int tile_step(const Seg &s) { return s.two ? 1 : 2; }
 __device__ __forceinline__ int end_tile(const Seg &s, int q) { return s.two && q == 0 ? s.n0 : s.n; }
 __device__ __forceinline__ bool has_tiles(const Seg &s, int q) { return first_tile(s, q) < end_tile(s, q); }
 
+// The segments go through a short ring in shared memory: one warp finds
+// them (its 64-bit divisions and counts would otherwise take registers and
+// instruction cache in every role), the others read.  A segment of no tiles is the end.
+template <int kSegs>
+struct SegRing {
+  static constexpr int kDepth = kSegs;
+  Seg seg[kDepth];
+  uint64_t full[kDepth], empty[kDepth];
+};
+template <int kSegs>
+__device__ __forceinline__ void init_seg_ring(SegRing<kSegs> &r, int readers) {
+  for (int i = 0; i < kSegs; ++i) {
+    mbar_init(smem_u32(&r.full[i]), 1);
+    mbar_init(smem_u32(&r.empty[i]), readers);
+  }
+}
+// A reading warp: get() waits for the next segment, done() lets it go.
+template <class Segs>
+struct SegReader {
+  Ring<Segs::kDepth> r;
+  __device__ __forceinline__ bool get(Segs &ring, const WaitCtx &w) {
+    return warp_wait(smem_u32(&ring.full[r.slot]), r.phase, w);
+  }
+  __device__ __forceinline__ const Seg &seg(const Segs &ring) const { return ring.seg[r.slot]; }
+  __device__ __forceinline__ void done(Segs &ring) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ring.empty[r.slot]));
+    r.next();
+  }
+};
+
 __device__ __forceinline__ void init_barriers(Smem &sm, bool cache) {
   for (int q = 0; q < 2; ++q) {
     mbar_init(smem_u32(&sm.q_full[q]), cache ? 4 : 1);
     mbar_init(smem_u32(&sm.s_full[q]), 1);
+    mbar_init(smem_u32(&sm.q_free[q]), 1);
     mbar_init(smem_u32(&sm.p_full[q]), 4);
   }
   for (int s = 0; s < kNK; ++s) {
@@ -135,29 +165,6 @@ __device__ __forceinline__ void init_barriers(Smem &sm, bool cache) {
   fence_mbar_init();
 }
 
-// Sum of the values of the threads before this one, and of all.
-__device__ __forceinline__ int64_t block_prefix(Smem &sm, int64_t v, int64_t *total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t inc = v;
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
-    if (lane >= x) inc += o;
-  }
-  __syncthreads();
-  if (lane == 31) sm.warp_sum[warp] = inc;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t t = sm.warp_sum[w];
-    before += w < warp ? t : 0;
-    all += t;
-  }
-  *total = all;
-  return before + inc - v;
-}
-
 // ------------------------------------------------------------- MMA issuer --
 // The warp runs this converged; one elected lane issues.  Order per key tile
 // and stream: PV of the tile, then QK of the stream's next tile, so that the
@@ -168,6 +175,7 @@ struct MmaState {
   Ring<kNV> v;
   uint32_t p_phase[2] = {0, 0};
   uint32_t q_phase[2] = {0, 0};
+  uint32_t fix_phase = 0;
 };
 
 __device__ __forceinline__ void mma_setup(MmaState &m, Smem &sm, bool bf16) {
@@ -200,15 +208,16 @@ __device__ __forceinline__ void issue_pv(const MmaState &m, int q, int vs, bool 
 }
 
 // One segment's products.  kReady: tiles are handed over by the dequantising
-// warps (k_ready, v_ready); otherwise by the copies (k_load, v_load), and a
-// ragged last V tile by v_fixed.
+// warps (k_ready, v_ready); otherwise by the copies (k_load, v_load), a ragged
+// last V tile goes through the warps that zero its rest (v_tail, v_fixed), and
+// the Q tiles are let go (q_free).
 template <bool kReady>
 __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s, bool ragged, const WaitCtx &w) {
   uint64_t *k_rdy = kReady ? sm.k_ready : sm.k_load;
   uint64_t *v_rdy = kReady ? sm.v_ready : sm.v_load;
   // the stream's QK of tile t: waits for the tile (its first user does), and
   // releases it after its last user
-  auto qk = [&](int q, bool first_user, bool last_user) {
+  auto qk = [&](int q, bool first_user, bool last_user, bool last_qk) {
     if (first_user) {
       if (!warp_wait(smem_u32(&k_rdy[m.k.slot]), m.k.phase, w)) return false;
       tc_fence_after();
@@ -219,6 +228,7 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
       mma_commit(m.go, smem_u32(&sm.k_free[m.k.slot]));
       m.k.next();
     }
+    if (!kReady && last_qk) mma_commit(m.go, smem_u32(&sm.q_free[q]));
     return true;
   };
   for (int q = 0; q < 2; ++q) {
@@ -228,13 +238,18 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
     tc_fence_after();
     // two: both streams start on tile 0 (stream 1 alone where stream 0 has none)
     const bool first_user = !s.two || q == 0 || s.n0 == 0;
-    if (!qk(q, first_user, !s.two || q == 1)) return false;
+    if (!qk(q, first_user, !s.two || q == 1, first_tile(s, q) + tile_step(s) >= end_tile(s, q))) return false;
   }
   const int step = tile_step(s);
   for (int t = 0; t < s.n; ++t) {
-    const bool fixed = !kReady && ragged && t == s.n - 1;
-    if (!warp_wait(fixed ? smem_u32(&sm.v_fixed) : smem_u32(&v_rdy[m.v.slot]), fixed ? 0u : m.v.phase, w))
-      return false;
+    if (!warp_wait(smem_u32(&v_rdy[m.v.slot]), m.v.phase, w)) return false;
+    if (!kReady && ragged && t == s.n - 1) {
+      // (the rows' softmax of this tile still runs)
+      if (m.go) mbar_arrive(smem_u32(&sm.v_tail));
+      __syncwarp();
+      if (!warp_wait(smem_u32(&sm.v_fixed), m.fix_phase, w)) return false;
+      m.fix_phase ^= 1u;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int q = s.two ? i : (t & 1);
@@ -248,7 +263,7 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
       const int tn = t + step;
       if (tn < end_tile(s, q)) {
         const bool first_user = !s.two || q == 0 || tn >= s.n0;
-        if (!qk(q, first_user, !s.two || q == 1)) return false;
+        if (!qk(q, first_user, !s.two || q == 1, tn + step >= end_tile(s, q))) return false;
       }
     }
     m.v.next();
@@ -336,10 +351,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool firs
 }
 
 // Columns below `n` of a 128-column tile, as bits.
-__device__ __forceinline__ void prefix_mask(int64_t n, uint32_t (&see)[4]) {
+__device__ __forceinline__ void prefix_mask(int32_t n, uint32_t (&see)[4]) {
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const int64_t k = n - 32 * g;
+    const int32_t k = n - 32 * g;
     see[g] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
   }
 }

@@ -212,25 +212,14 @@ struct Walk {
   }
 };
 
-// The segments go through a short ring in shared memory: one warp walks (its
-// 64-bit divisions and counts would otherwise take registers and instruction
-// cache in every role), the others read.  A segment of no tiles is the end.
-struct SegRing {
-  static constexpr int kDepth = 4;
-  Seg seg[kDepth];
-  uint64_t full[kDepth], empty[kDepth];
-};
-__device__ __forceinline__ void init_seg_ring(SegRing &r, int readers) {
-  for (int i = 0; i < SegRing::kDepth; ++i) {
-    mbar_init(smem_u32(&r.full[i]), 1);
-    mbar_init(smem_u32(&r.empty[i]), readers);
-  }
-}
+using TreeSegs = SegRing<4>;
+using TreeReader = SegReader<TreeSegs>;
+
 // The walking warp.
-__device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &sc, SegRing &ring, const WaitCtx &w) {
+__device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &sc, TreeSegs &ring, const WaitCtx &w) {
   Walk walk;
   walk.start(a, sc);
-  Ring<SegRing::kDepth> r;
+  Ring<TreeSegs::kDepth> r;
   for (;;) {
     Seg s;
     const bool more = walk.next(a, &s);
@@ -244,20 +233,6 @@ __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &
     r.next();
   }
 }
-// A reading warp: get() waits for the next segment, done() lets it go.
-struct SegReader {
-  Ring<SegRing::kDepth> r;
-  __device__ __forceinline__ bool get(SegRing &ring, const WaitCtx &w) {
-    return warp_wait(smem_u32(&ring.full[r.slot]), r.phase, w);
-  }
-  __device__ __forceinline__ const Seg &seg(const SegRing &ring) const { return ring.seg[r.slot]; }
-  __device__ __forceinline__ void done(SegRing &ring) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ring.empty[r.slot]));
-    r.next();
-  }
-};
-
 // The node of row x of a sequence and kv head: x / group by a multiply and a
 // shift, exact for x below 64 * 64 (the error is below 2^-7, group at most 64).
 __device__ __forceinline__ int node_of(const TreeArgs &a, int x) {
