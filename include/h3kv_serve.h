@@ -87,8 +87,8 @@ h3kv_status h3kv_paged_keep(const h3kv_paged_store *store, const int32_t *page_t
                             const int32_t *lengths, const int32_t *cu_nodes, int32_t seqs, const uint8_t *keep,
                             int64_t nodes, int32_t *new_lengths, void *stream);
 
-/* Device bytes of h3kv_attend_tree's workspace (0 for invalid arguments).
- * It needs no initial value; calls that overlap on the GPU (two streams, two
+/* Device bytes of h3kv_attend_tree's workspace (0 for invalid arguments),
+ * which is 32-byte aligned.  It needs no initial value; calls that overlap on the GPU (two streams, two
  * replayed graphs) must not share it. */
 size_t h3kv_attend_tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs);
 

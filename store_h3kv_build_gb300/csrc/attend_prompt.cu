@@ -23,7 +23,6 @@ constexpr uint32_t kRegRows = 208, kRegZero = 40, kRegCopy = 56;
 static_assert(2 * kRegRows + kRegZero + kRegCopy == 512, "register split");
 
 struct PromptSmem : Smem {
-  float2 ml[kBM];  // stream 1's (max, sum) for the join with stream 0
   PromptSegs segs;
   alignas(16) uint64_t taken[2];  // answer of a request for another block
   uint64_t taken_bar;

@@ -1,7 +1,6 @@
 // attend_tree.cu -- attention of drafted tokens over the paged kvi8r cache: the
 // kernel for many rows of a sequence and kv head (the tcgen05 pipeline of
 // serve_attend.cuh), the join, and the choice of kernel.
-#include "store_fwht.cuh"
 #include "tree.cuh"
 
 namespace h3kv {
@@ -64,6 +63,47 @@ __device__ __forceinline__ void produce(const TreeArgs &a, TreeSmem &sm, uint8_t
   }
 }
 
+// q' = fp16(q H) of 32 rows of a segment, from row w0 on, into rows t0 .. of the
+// swizzled K-major tile; zeros behind the segment's rows.  One warp: 8 lanes
+// hold a row (values 8l .. 8l+7 and 64 + 8l .. of it), 4 rows at a time.  The
+// rows are copied as they are to the places where the same lanes then write
+// them rotated.  Loops that are not unrolled: instructions that run once a
+// segment are waited for (unrolled, this took 10 us).
+__device__ __forceinline__ void rotate_rows(const TreeArgs &a, const Seg &s, uint8_t *tile, int w0, int t0) {
+  const int lane = threadIdx.x & 31, l = lane & 7, ti = t0 + (lane >> 3);
+  if (w0 < s.rows) {
+#pragma unroll 1
+    for (int it = 0; it < 8; ++it) {
+      const int row = w0 + it * 4 + (lane >> 3);
+      const bool in = row < s.rows;
+      const int x = s.row0 + (in ? row : 0), node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
+      const uint16_t *src = a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride + 8 * l;
+      const uint32_t dst = smem_u32(tile) + sw128_off(ti + 4 * it, l);
+      copy16_async(dst, src, in);
+      copy16_async(dst + kChunkBytes, src + 64, in);
+    }
+    copy16_wait();
+#pragma unroll 1
+    for (int it = 0; it < 8 && w0 + it * 4 < s.rows; ++it) {
+      uint4 *lo = reinterpret_cast<uint4 *>(tile + sw128_off(ti + 4 * it, l));
+      uint4 *hi = reinterpret_cast<uint4 *>(tile + kChunkBytes + sw128_off(ti + 4 * it, l));
+      float v[16];
+      unpack_bf16x8(*lo, v);
+      unpack_bf16x8(*hi, v + 8);
+      fwht128_oct(v, l);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] *= kInvSqrt128;
+      *lo = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                       pack_f16x2(v[6], v[7]));
+      *hi = make_uint4(pack_f16x2(v[8], v[9]), pack_f16x2(v[10], v[11]), pack_f16x2(v[12], v[13]),
+                       pack_f16x2(v[14], v[15]));
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   TreeSmem &sm = *reinterpret_cast<TreeSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -72,8 +112,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
 
   // the join may start its CTAs; it waits there until this grid is done
   if (tid == 0) pdl_launch_dependents();
-  find_run<kThreads>(a, ws, sm.scan);
-  if (sm.scan.u0 >= sm.scan.u1) return;
+  find_run<kThreads>(a, sm.scan, reinterpret_cast<int64_t *>(sm.q[0]));
+  if (sm.scan.u0 >= sm.scan.u1) {
+    if (tid == 0) ws.split[blockIdx.x].parts = 0;
+    return;
+  }
 
   if (tid == 0) {
     init_seg_ring(sm.segs, 15);
@@ -99,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     const float c2 = a.scale_log2;
     const int i = tid & 127;
     uint32_t s_phase = 0, o_phase = 0;
+    bool first = true;
     for (;;) {
       // the eight warps go on, or leave, together
       if (!named_bar_and(1, 256, sr.get(sm.segs, w))) break;
@@ -108,50 +152,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const int r = base_row + i;
       const int w0 = base_row + (warp & 3) * 32;  // the warp's first row
       const bool warp_on = w0 < s.rows;
-      // q' = fp16(q H) into the swizzled K-major tile, which is free: this
-      // stream's last QK of the segment before has completed.  A thread takes
-      // its own row: H128 = [[H64, H64], [H64, -H64]], so half hf of the
-      // rotated row is H64 of the sum (hf 0) or difference (hf 1) of the row's
-      // halves, 64 values in registers and no shuffles (with a row over 8
-      // lanes they took most of 5 us); a loop over hf, since instructions that
-      // run once a segment are waited for.
-      if (has_tiles(s, q)) {
-        if (warp_on) {
-          uint4 raw[16];
-          const int x = s.row0 + r, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
-          const uint4 *src =
-              reinterpret_cast<const uint4 *>(a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride);
-#pragma unroll
-          for (int g = 0; g < 16; ++g) raw[g] = r < s.rows ? __ldg(src + g) : make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            const float2 sign = hf ? make_float2(-1.f, -1.f) : make_float2(1.f, 1.f);
-            float v[64];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              float lo[8], hi[8];
-              unpack_bf16x8(raw[g], lo);
-              unpack_bf16x8(raw[8 + g], hi);
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                const float2 y = __ffma2_rn(make_float2(hi[e], hi[e + 1]), sign, make_float2(lo[e], lo[e + 1]));
-                v[8 * g + e] = y.x;
-                v[8 * g + e + 1] = y.y;
-              }
-            }
-            fwht64_packed(v);
-#pragma unroll
-            for (int e = 0; e < 64; ++e) v[e] *= kInvSqrt128;
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-              *reinterpret_cast<uint4 *>(sm.q[q] + hf * kChunkBytes + sw128_off(i, g)) =
-                  make_uint4(pack_f16x2(v[8 * g], v[8 * g + 1]), pack_f16x2(v[8 * g + 2], v[8 * g + 3]),
-                             pack_f16x2(v[8 * g + 4], v[8 * g + 5]), pack_f16x2(v[8 * g + 6], v[8 * g + 7]));
-          }
+      if (first) {
+        // nobody is busy yet: every warp rotates its own rows
+        first = false;
+        if (has_tiles(s, q)) {
+          rotate_rows(a, s, sm.q[q], w0, (warp & 3) * 32);
+          if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[q]));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[q]));
       }
       const int32_t base_key = static_cast<int32_t>(s.keys) - s.nodes, pos0 = s.t0 * kBN;
       uint64_t path = 0;
@@ -184,60 +191,57 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       ok = ok && warp_wait(smem_u32(&sm.o_full), o_phase, w);
       o_phase ^= 1u;
       tc_fence_after();
-      if (!s.two && q == 1) join_ml(sm)[i] = make_float2(row.m, row.l);
+      if (!s.two && q == 1) sm.ml[i] = make_float2(row.m, row.l);
       ok = named_bar_and(1, 256, ok);
       if (!ok) break;
       if ((s.two || q == 0) && warp_on) {
         const bool joined = !s.two && s.n > 1;
         float ga = 1.f, gb = 0.f;
-        if (joined) join_rows(row, join_ml(sm)[i], c2, ga, gb);
-        // the rows go out through this stream's Q tile (free until the next
-        // segment's rows are written), 16-byte granule g of a row at
-        // g ^ (row mod 16), so that a warp writes whole rows
-        float o[128];
-        uint8_t *stage = sm.q[q] + i * 256;
-        const int g = lane & 15;
-        const float inv = s.whole ? kInvSqrt128 / row.l : 1.f;
-        load_o(tO, tO + 128, joined, ga * inv, gb * inv, o);
+        if (joined) join_rows(row, sm.ml[i], c2, ga, gb);
+        const bool live = r < s.rows;
         if (s.whole) {
+          float o[128];
+          const float inv = kInvSqrt128 / row.l;
+          load_o(tO, tO + 128, joined, ga * inv, gb * inv, o);
           fwht128_packed(o);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            *reinterpret_cast<uint4 *>(stage + ((k ^ (i & 15)) << 4)) =
-                make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                           pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-          __syncwarp();
-          for (int rr = 0; rr < 32; rr += 2) {
-            const int ti = rr + (lane >> 4);
-            if (w0 + ti < s.rows) {
-              const int x = s.row0 + w0 + ti, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
-              const int sr_row = (warp & 3) * 32 + ti;
-              *reinterpret_cast<uint4 *>(a.o.data + h * a.o.head_stride + (s.q_base + node) * a.o.row_stride + g * 8) =
-                  *reinterpret_cast<const uint4 *>(sm.q[q] + sr_row * 256 + ((g ^ (sr_row & 15)) << 4));
-            }
-          }
-          if (a.lse && r < s.rows) {
+          if (live) {
             const int x = s.row0 + r, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
-            a.lse[h * a.nodes + s.q_base + node] = kLn2 * (row.m * c2 + log2f(row.l));
+            uint16_t *dst = a.o.data + h * a.o.head_stride + (s.q_base + node) * a.o.row_stride;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              uint32_t c[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) c[k] = pack_bf16x2(o[16 * g + 2 * k], o[16 * g + 2 * k + 1]);
+              if constexpr (kWide) {
+                st_global_v8(dst + 16 * g, c);
+              } else {
+                reinterpret_cast<uint4 *>(dst)[2 * g] = make_uint4(c[0], c[1], c[2], c[3]);
+                reinterpret_cast<uint4 *>(dst)[2 * g + 1] = make_uint4(c[4], c[5], c[6], c[7]);
+              }
+            }
+            if (a.lse) a.lse[h * a.nodes + s.q_base + node] = kLn2 * (row.m * c2 + log2f(row.l));
           }
         } else {
-          const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (s.t0 > 0 ? 0 : 1)) * ws.rows;
+          const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (s.t0 > 0 ? 0 : 1)) * ws.rows + r;
+          float *dst = ws.o + at * 128;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float x[16];
+            tmem_ld16(tO + c * 16, *reinterpret_cast<uint32_t(*)[16]>(x));
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+            for (int k = 0; k < 16; ++k) x[k] *= ga;
+            if (joined) {
+              float y[16];
+              tmem_ld16(tO + 128 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(y));
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              *reinterpret_cast<float4 *>(stage + ((k ^ (i & 15)) << 4)) =
-                  make_float4(o[64 * hf + 4 * k], o[64 * hf + 4 * k + 1], o[64 * hf + 4 * k + 2], o[64 * hf + 4 * k + 3]);
-            __syncwarp();
-            for (int rr = 0; rr < 32; rr += 2) {
-              const int ti = rr + (lane >> 4), sr_row = (warp & 3) * 32 + ti;
-              if (w0 + ti < s.rows)
-                *reinterpret_cast<float4 *>(ws.o + (at + w0 + ti) * 128 + 64 * hf + 4 * g) =
-                    *reinterpret_cast<const float4 *>(sm.q[q] + sr_row * 256 + ((g ^ (sr_row & 15)) << 4));
+              for (int k = 0; k < 16; ++k) x[k] = fmaf(y[k], gb, x[k]);
             }
-            __syncwarp();
+            if (live) {
+              st_global_v8(dst + 16 * c, *reinterpret_cast<const uint32_t(*)[8]>(x));
+              st_global_v8(dst + 16 * c + 8, *reinterpret_cast<const uint32_t(*)[8]>(x + 8));
+            }
           }
-          if (r < s.rows) ws.ml[at + r] = make_float2(row.m, row.l);
+          if (live) ws.ml[at] = make_float2(row.m, row.l);
         }
       }
       // stream 1's O and (max, sum) have been read
@@ -258,15 +262,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       fence_proxy_async_smem();
       __syncwarp();
     };
-    bool ok = true;
+    uint32_t q_phase[2] = {0, 0};
+    bool ok = true, first = true;
     while (ok && (ok = sr.get(sm.segs, w))) {
       const Seg &s = sr.seg(sm.segs);
       const int n = s.n, head = s.head;
       const int64_t table = s.k_base;
       const int32_t keys = static_cast<int32_t>(s.keys);
       int32_t pos = s.t0 * kBN + dw * 32;  // the warp's first row
-      sr.done(sm.segs);
       if (n == 0) break;
+      // the query rows of every segment but the first (see rotate_rows): the
+      // softmax warps are then still at the output of the one before
+      for (int q = 0; q < 2; ++q) {
+        if (!has_tiles(s, q)) continue;
+        q_phase[q] ^= 1u;
+        if (first) continue;
+        if (!(ok = warp_wait(smem_u32(&sm.q_free[q]), q_phase[q], w))) break;
+        rotate_rows(a, s, sm.q[q], (s.two ? q * kBM : 0) + dw * 32, dw * 32);
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[q]));
+      }
+      first = false;
+      sr.done(sm.segs);
+      if (!ok) break;
       // the pages of its rows 0-15 and 16-31, read one tile ahead
       const int ps = a.p.page_size;
       auto pages_of = [&](int32_t p, int32_t (&pg)[2]) {
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mma_commit(m.go, smem_u32(&sm.drain));
       mbar_wait_drain(smem_u32(&sm.drain), 0, kDrainNs);
     } else if (warp == 15) {
-      publish_segments(a, sm.scan, sm.segs, w);
+      publish_segments(a, sm.scan, ws, sm.segs, w);
     }
   }
   __syncwarp();
@@ -332,59 +349,83 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   }
 }
 
-// Joins the items that lie on several CTAs: CTA column b takes the item that the
-// b-th CTA goes on with, where that CTA is the item's second.  One warp for a
-// row: its parts in order, un-rotated and written.
-constexpr int kJoinWarps = 8;
+// Joins the items that lie on several CTAs: block column b takes the one that
+// CTA b is the second of.  A warp takes 4 rows; where an item has fewer rows
+// than the block's 8 warps hold, the warps share its parts (warp w of `ways`
+// takes parts w, w + ways, ..) and meet in shared memory.  Parts are added in a
+// fixed order.
+constexpr int kJoinWarps = 8, kJoinRows = 4;
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a) {
-  const int lane = threadIdx.x & 31, b = blockIdx.x + 1;
+  __shared__ float4 sh_o[kJoinWarps][kJoinRows][32];
+  __shared__ float2 sh_ml[kJoinWarps][kJoinRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x + 1;
   // (no thread leaves before this, so the grids end in stream order)
   pdl_wait_prerequisites();
   const Workspace ws = workspace_of(a);
-  const int64_t total = ws.prefix[a.seqs];
-  const int ctas = working(a, total);
-  if (b >= ctas) return;
-  const int64_t u = first_unit(total, b, ctas);
-  // the sequence that holds unit u: the last with prefix <= u (those without
-  // work share theirs with the next)
-  int lo = 0, hi = a.seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (ws.prefix[mid] <= u) lo = mid;
-    else hi = mid - 1;
+  const Split sp = ws.split[b];
+  if (sp.parts == 0) return;
+  const int groups = ws.rows <= 4 ? 1 : ws.rows <= 8 ? 2 : ws.rows <= 16 ? 4 : 8, ways = kJoinWarps / groups;
+  const int g = warp % groups, way = warp / groups;
+  const int r0 = (blockIdx.y * groups + g) * kJoinRows;
+  const float c2 = a.scale_log2;
+  float m[kJoinRows], l[kJoinRows];
+  float4 o[kJoinRows];
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i) {
+    m[i] = kNoMax;
+    l[i] = 0.f;
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const Counts c = counts_of(a, lo);
-  const int size = c.tiles + a.item_cost;
-  const int64_t item = (u - ws.prefix[lo]) / size;
-  // its tiles' units, and the first CTA that has one
-  const int64_t u0 = ws.prefix[lo] + item * size + a.item_cost, u1 = u0 + c.tiles;
-  if (u <= u0 || first_unit(total, b - 1, ctas) > u0) return;
-  const int head = static_cast<int>(item / c.row_tiles);
-  const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * c.row_tiles) * a.item_rows;
-  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  const int x = row0 + r;
-  if (r >= a.item_rows || x >= c.nodes * a.group) return;
-  float m = kNoMax, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = b - 1; k < ctas && first_unit(total, k, ctas) < u1; ++k) {
-    const int64_t at = (static_cast<int64_t>(k) * 2 + (k == b - 1 ? 1 : 0)) * ws.rows + r;
-    const float2 ml = ws.ml[at];
-    const float4 p = reinterpret_cast<const float4 *>(ws.o + at * 128)[lane];
-    const float mn = fmaxf(m, ml.x);
-    const float ga = ex2((m - mn) * a.scale_log2), gb = ex2((ml.x - mn) * a.scale_log2);
-    l = fmaf(l, ga, ml.y * gb);
-    o[0] = fmaf(o[0], ga, p.x * gb);
-    o[1] = fmaf(o[1], ga, p.y * gb);
-    o[2] = fmaf(o[2], ga, p.z * gb);
-    o[3] = fmaf(o[3], ga, p.w * gb);
-    m = mn;
+  auto add = [&](int i, float2 ml, float4 p) {
+    const float mn = fmaxf(m[i], ml.x), ga = ex2((m[i] - mn) * c2), gb = ex2((ml.x - mn) * c2);
+    l[i] = fmaf(l[i], ga, ml.y * gb);
+    o[i].x = fmaf(o[i].x, ga, p.x * gb);
+    o[i].y = fmaf(o[i].y, ga, p.y * gb);
+    o[i].z = fmaf(o[i].z, ga, p.z * gb);
+    o[i].w = fmaf(o[i].w, ga, p.w * gb);
+    m[i] = mn;
+  };
+#pragma unroll 2
+  for (int k = way; k < sp.parts; k += ways) {
+    const int64_t at = (static_cast<int64_t>(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * ws.rows + r0;
+    float2 ml[kJoinRows];
+    float4 p[kJoinRows];
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      if (r0 + i < sp.rows) {
+        ml[i] = ws.ml[at + i];
+        p[i] = reinterpret_cast<const float4 *>(ws.o + (at + i) * 128)[lane];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i)
+      if (r0 + i < sp.rows) add(i, ml[i], p[i]);
   }
-  fwht128_warp(o, lane);
-  const float inv = kInvSqrt128 / l;
-  const int node = node_of(a, x), h = head * a.group + (x - node * a.group);
-  const int64_t row = c.q_base + node;
-  *reinterpret_cast<uint2 *>(a.o.data + h * a.o.head_stride + row * a.o.row_stride + 4 * lane) =
-      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  if (a.lse && lane == 0) a.lse[h * a.nodes + row] = kLn2 * (m * a.scale_log2 + log2f(l));
+  if (ways > 1) {
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      sh_o[warp][i][lane] = o[i];
+      if (lane == 0) sh_ml[warp][i] = make_float2(m[i], l[i]);
+    }
+    __syncthreads();
+    if (way > 0) return;
+    for (int x = 1; x < ways; ++x) {
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i) add(i, sh_ml[x * groups + g][i], sh_o[x * groups + g][i][lane]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i) {
+    if (r0 + i >= sp.rows) break;
+    float v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+    fwht128_warp(v, lane);
+    const float inv = kInvSqrt128 / l[i];
+    const int x = sp.row0 + r0 + i, node = node_of(a, x), h = sp.head * a.group + (x - node * a.group);
+    const int64_t row = sp.q_base + node;
+    *reinterpret_cast<uint2 *>(a.o.data + h * a.o.head_stride + row * a.o.row_stride + 4 * lane) =
+        make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+    if (a.lse && lane == 0) a.lse[h * a.nodes + row] = kLn2 * (m[i] * c2 + log2f(l[i]));
+  }
 }
 
 }  // namespace
@@ -393,7 +434,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a)
 size_t tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs) {
   const int32_t group = q_heads / kv_heads;
   const size_t rows = serve::part_rows(group, nodes, serve::item_rows_of(group, nodes, seqs));
-  return serve::prefix_bytes(seqs) + serve::kMaxCtas * 2 * rows * (128 * sizeof(float) + sizeof(float2));
+  return serve::kMaxCtas * (sizeof(serve::Split) + 2 * rows * (128 * sizeof(float) + sizeof(float2)));
 }
 
 cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
@@ -407,17 +448,21 @@ cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
   if (a.item_rows < kManyRows) {
     e = launch_tree_few(a, stream);
   } else {
-    e = cudaFuncSetAttribute(tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kTreeSmemBytes));
+    // whole 32-byte sectors per store where the output's alignment allows
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.o.data) | static_cast<uintptr_t>(a.o.head_stride * 2) |
+                        static_cast<uintptr_t>(a.o.row_stride * 2)) &
+                       31) == 0;
+    auto kernel = wide ? tree_kernel<true> : tree_kernel<false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTreeSmemBytes));
     if (e != cudaSuccess) return e;
-    tree_kernel<<<a.ctas, kThreads, kTreeSmemBytes, stream>>>(a);
+    kernel<<<a.ctas, kThreads, kTreeSmemBytes, stream>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
   if (a.ctas < 2) return cudaSuccess;
   const int rows = part_rows(a.group, a.nodes, a.item_rows);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas - 1, (rows + kJoinWarps - 1) / kJoinWarps);
+  cfg.gridDim = dim3(a.ctas - 1, (rows + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

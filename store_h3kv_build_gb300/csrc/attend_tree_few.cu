@@ -89,14 +89,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     sm.abort = 0;
     fence_mbar_init();
   }
-  find_run<kFewThreads>(a, ws, sm.scan);
-  if (sm.scan.u0 >= sm.scan.u1) return;
+  find_run<kFewThreads>(a, sm.scan, reinterpret_cast<int64_t *>(sm.o));
+  if (sm.scan.u0 >= sm.scan.u1) {
+    if (tid == 0) ws.split[blockIdx.x].parts = 0;
+    return;
+  }
   const WaitCtx w{a.p.err, &sm.abort, a.timeout_ns};
 
   TreeReader sr;
 
   if (warp == kWarps + kProducers) {
-    publish_segments(a, sm.scan, sm.segs, w);
+    publish_segments(a, sm.scan, ws, sm.segs, w);
     return;
   }
   if (warp >= kWarps) {

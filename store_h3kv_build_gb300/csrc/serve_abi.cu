@@ -168,7 +168,7 @@ h3kv_status h3kv_attend_tree(const h3kv_rows *Q, int32_t q_heads, int64_t nodes,
   if (!lengths || !cu_nodes || !aligned(lengths, 4) || !aligned(cu_nodes, 4) || !aligned(parents, 4) ||
       !aligned(lse, 4))
     return H3KV_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 16) ||
+  if (!workspace || !aligned(workspace, 32) ||
       workspace_bytes < h3kv::tree_workspace_bytes(q_heads, a.p.kv_heads, nodes, seqs))
     return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;

@@ -55,20 +55,17 @@ struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kNK][kTileBytes];
   uint8_t v[kNV][kTileBytes];
+  float2 ml[kBM];  // stream 1's (max, sum) for the join with stream 0
   uint64_t q_full[2];
   uint64_t k_load[kNK], k_ready[kNK], k_free[kNK];
   uint64_t v_load[kNV], v_ready[kNV], v_free[kNV];
   uint64_t s_full[2], p_full[2];
   uint64_t o_full, drain;
-  uint64_t q_free[2];        // prompts: the stream's last QK of a segment is done
+  uint64_t q_free[2];        // the stream's last QK of a segment is done
   uint64_t v_tail, v_fixed;  // prompts: a ragged last V tile has come; its rest is zeroed
   uint32_t tmem_base;
   int abort;
 };
-// Stream 1's (max, sum) for the join with stream 0 lie in its Q tile, which is
-// free once the segment's products are done.
-__device__ __forceinline__ float2 *join_ml(Smem &sm) { return reinterpret_cast<float2 *>(sm.q[1]); }
-
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -208,9 +205,10 @@ __device__ __forceinline__ void issue_pv(const MmaState &m, int q, int vs, bool 
 }
 
 // One segment's products.  kReady: tiles are handed over by the dequantising
-// warps (k_ready, v_ready); otherwise by the copies (k_load, v_load), a ragged
-// last V tile goes through the warps that zero its rest (v_tail, v_fixed), and
-// the Q tiles are let go (q_free).
+// warps (k_ready, v_ready); otherwise by the copies (k_load, v_load), and a
+// ragged last V tile goes through the warps that zero its rest (v_tail,
+// v_fixed).  A stream's Q tile is let go (q_free) after its last QK, so that
+// the next segment's rows come in under this one's end.
 template <bool kReady>
 __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s, bool ragged, const WaitCtx &w) {
   uint64_t *k_rdy = kReady ? sm.k_ready : sm.k_load;
@@ -228,7 +226,7 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
       mma_commit(m.go, smem_u32(&sm.k_free[m.k.slot]));
       m.k.next();
     }
-    if (!kReady && last_qk) mma_commit(m.go, smem_u32(&sm.q_free[q]));
+    if (last_qk) mma_commit(m.go, smem_u32(&sm.q_free[q]));
     return true;
   };
   for (int q = 0; q < 2; ++q) {

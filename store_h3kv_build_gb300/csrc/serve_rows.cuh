@@ -14,6 +14,13 @@ __device__ __forceinline__ void ld_global_v8(const void *p, uint4 &a, uint4 &b) 
                : "l"(p));
 }
 
+// 16 bytes from global to shared memory without a register; zeros where !in.
+// copy16_wait: this thread's copies are done.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void unpack_bf16x8(const uint4 w, float *x) {
   x[0] = bf16lo_to_f32(w.x);
   x[1] = bf16hi_to_f32(w.x);

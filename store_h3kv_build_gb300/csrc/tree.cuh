@@ -30,27 +30,33 @@ inline int item_rows_of(int32_t group, int64_t nodes, int32_t seqs) {
   return mean <= 8 ? 8 : mean <= 16 ? 16 : kManyRows;
 }
 
-// Workspace: prefix of units before each sequence (int64 [seqs + 1]), then
-// per CTA and part (max, sum) [rows] and un-normalised O [rows][128].
+// An item that lies on several CTAs, as the second of them describes it to the
+// join.
+struct Split {
+  int64_t q_base;
+  int32_t parts;  // CTAs that hold its tiles, from the one before on; 0: none
+  int32_t head, row0, rows;
+  int32_t pad[2];
+};
+
+// Workspace: a Split per CTA, then per CTA and part un-normalised O
+// [rows][128] and (max, sum) [rows].
 struct Workspace {
-  int64_t *prefix;
-  float2 *ml;
+  Split *split;
   float *o;
+  float2 *ml;
   int rows;  // rows of a part
 };
 __host__ __device__ inline int part_rows(int group, int64_t nodes, int item_rows) {
   const int64_t n = group * (nodes < H3KV_TREE_MAX_NODES ? nodes : H3KV_TREE_MAX_NODES);
   return n < item_rows ? static_cast<int>(n) : item_rows;
 }
-__host__ __device__ inline size_t prefix_bytes(int32_t seqs) {
-  return (static_cast<size_t>(seqs + 1) * 8 + 255) / 256 * 256;
-}
 __device__ inline Workspace workspace_of(const TreeArgs &a) {
   Workspace ws;
   uint8_t *p = reinterpret_cast<uint8_t *>(a.workspace);
   ws.rows = part_rows(a.group, a.nodes, a.item_rows);
-  ws.prefix = reinterpret_cast<int64_t *>(p);
-  ws.o = reinterpret_cast<float *>(p + prefix_bytes(a.seqs));
+  ws.split = reinterpret_cast<Split *>(p);
+  ws.o = reinterpret_cast<float *>(p + kMaxCtas * sizeof(Split));
   ws.ml = reinterpret_cast<float2 *>(ws.o + static_cast<int64_t>(a.ctas) * 2 * ws.rows * 128);
   return ws;
 }
@@ -87,18 +93,23 @@ __device__ __forceinline__ int working(const TreeArgs &a, int64_t total) {
   return total < a.ctas ? static_cast<int>(total) : a.ctas;
 }
 __device__ __forceinline__ int64_t first_unit(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+// The CTA that holds unit u: the last k with total k / ctas < u + 1.
+__device__ __forceinline__ int owner_of(int64_t total, int64_t u, int ctas) {
+  return static_cast<int>(((u + 1) * ctas - 1) / total);
+}
 
 // This CTA's run of units: found by all threads of the block, kept in shared
-// memory.  CTA 0 also checks every sequence and writes the prefix array.
+// memory (scratch: 32 words there).  CTA 0 also checks every sequence.
 struct Scan {
+  int64_t total;
   int64_t u0, u1;
   int64_t before;  // units before sequence `seq`, which holds unit u0
-  int seq;
-  int64_t warp_sum[32];
+  Counts c;        // of that sequence
+  int seq, ctas;
 };
 
 template <int kBlock>
-__device__ __forceinline__ int64_t block_prefix(int64_t (&warp_sum)[32], int64_t v, int64_t *total) {
+__device__ __forceinline__ int64_t block_prefix(int64_t *warp_sum, int64_t v, int64_t *total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t inc = v;
 #pragma unroll
@@ -121,30 +132,30 @@ __device__ __forceinline__ int64_t block_prefix(int64_t (&warp_sum)[32], int64_t
 }
 
 template <int kBlock>
-__device__ __forceinline__ void find_run(const TreeArgs &a, const Workspace &ws, Scan &sc) {
+__device__ __forceinline__ void find_run(const TreeArgs &a, Scan &sc, int64_t *scratch) {
   const int tid = threadIdx.x;
   int64_t total = 0;
-  int64_t at = 0, n = 0;  // this thread's sequence: units before it, and its own
+  int64_t at = 0;  // units before this thread's sequence
+  Counts c = {};
   for (int base = 0; base < a.seqs; base += kBlock) {
     const int i = base + tid;
     int64_t all;
-    n = 0;
+    c = {};
     if (i < a.seqs) {
-      const Counts c = counts_of(a, i);
-      n = c.units;
+      c = counts_of(a, i);
       if (c.bad && blockIdx.x == 0) atomicOr(a.p.err, kErrIndex);
     }
-    at = total + block_prefix<kBlock>(sc.warp_sum, n, &all);
-    if (blockIdx.x == 0 && i < a.seqs) ws.prefix[i] = at;
+    at = total + block_prefix<kBlock>(scratch, c.units, &all);
     total += all;
   }
-  if (blockIdx.x == 0 && tid == 0) ws.prefix[a.seqs] = total;
   const int ctas = working(a, total), cta = static_cast<int>(blockIdx.x);
   const int64_t u0 = cta < ctas ? first_unit(total, cta, ctas) : total;
   const int64_t u1 = cta < ctas ? first_unit(total, cta + 1, ctas) : total;
   if (tid == 0) {
+    sc.total = total;
     sc.u0 = u0;
     sc.u1 = u1;
+    sc.ctas = ctas;
   }
   // the sequence that holds u0: known already where one round covered them all
   int64_t before = 0;
@@ -152,13 +163,15 @@ __device__ __forceinline__ void find_run(const TreeArgs &a, const Workspace &ws,
     if (a.seqs > kBlock) {
       const int i = base + tid;
       int64_t all;
-      n = i < a.seqs ? counts_of(a, i).units : 0;
-      at = before + block_prefix<kBlock>(sc.warp_sum, n, &all);
+      c = {};
+      if (i < a.seqs) c = counts_of(a, i);
+      at = before + block_prefix<kBlock>(scratch, c.units, &all);
       before += all;
     }
-    if (n > 0 && u0 >= at && u0 < at + n) {
+    if (c.units > 0 && u0 >= at && u0 < at + c.units) {
       sc.seq = base + tid;
       sc.before = at;
+      sc.c = c;
     }
     if (a.seqs > kBlock && u0 < before) break;
   }
@@ -176,7 +189,7 @@ struct Walk {
     end = sc.u1;
     seq = sc.seq;
     before = sc.before;
-    if (u < end) c = counts_of(a, seq);
+    c = sc.c;
   }
   __device__ __forceinline__ bool next(const TreeArgs &a, Seg *s) {
     while (u < end) {
@@ -212,13 +225,32 @@ struct Walk {
   }
 };
 
-using TreeSegs = SegRing<4>;
+using TreeSegs = SegRing<2>;
 using TreeReader = SegReader<TreeSegs>;
 
-// The walking warp.
-__device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &sc, TreeSegs &ring, const WaitCtx &w) {
+// The walking warp.  Where its first segment goes on with an item that began on
+// the CTA before, it describes the item to the join.
+__device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &sc, const Workspace &ws,
+                                                 TreeSegs &ring, const WaitCtx &w) {
   Walk walk;
   walk.start(a, sc);
+  Split split = {};
+  {
+    const int size = walk.c.tiles + a.item_cost;
+    const int64_t item = (walk.u - walk.before) / size;
+    // its tiles' units
+    const int64_t first = walk.before + item * size + a.item_cost, last = first + walk.c.tiles - 1;
+    const int cta = static_cast<int>(blockIdx.x);
+    if (walk.u > first && owner_of(sc.total, first, sc.ctas) == cta - 1) {
+      split.q_base = walk.c.q_base;
+      split.parts = owner_of(sc.total, last, sc.ctas) - cta + 2;
+      split.head = static_cast<int>(item / walk.c.row_tiles);
+      split.row0 = static_cast<int>(item - static_cast<int64_t>(split.head) * walk.c.row_tiles) * a.item_rows;
+      const int rows = walk.c.nodes * a.group - split.row0;
+      split.rows = rows < a.item_rows ? rows : a.item_rows;
+    }
+    if ((threadIdx.x & 31) == 0) ws.split[cta] = split;
+  }
   Ring<TreeSegs::kDepth> r;
   for (;;) {
     Seg s;
