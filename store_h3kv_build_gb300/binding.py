@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -502,16 +503,19 @@ def _need_strided(t, name: str, heads: int | None = None, rows: int | None = Non
         raise ValueError(f"{name}: {r} rows, expected {rows}")
     hs, rs, inner = t.stride()
     ptr = t.data_ptr()
-    if h and r:
-        if inner != 1:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
-        for d, n, st in ((0, h, hs), (1, r, rs)):
-            if n > 1 and (st % 8 != 0 or st < HEAD_DIM):
-                raise ValueError(f"{name}: stride {st} of dimension {d} must be a multiple of 8, at least {HEAD_DIM}")
-        if ptr % 16 != 0:
-            raise ValueError(f"{name}: must be 16-byte aligned")
+    if (inner != 1 or ptr % 16) and h and r:
+        raise ValueError(f"{name}: the last dimension must be contiguous" if inner != 1
+                         else f"{name}: must be 16-byte aligned")
     # the stride of a dimension of one entry is never used
-    return h3kv_rows(ptr, hs if h > 1 else 0, rs if r > 1 else 0)
+    if h <= 1:
+        hs = 0
+    elif (hs % 8 or hs < HEAD_DIM) and r:
+        raise ValueError(f"{name}: stride {hs} of dimension 0 must be a multiple of 8, at least {HEAD_DIM}")
+    if r <= 1:
+        rs = 0
+    elif (rs % 8 or rs < HEAD_DIM) and h:
+        raise ValueError(f"{name}: stride {rs} of dimension 1 must be a multiple of 8, at least {HEAD_DIM}")
+    return h3kv_rows(ptr, hs, rs)
 
 
 def _need_index(t, name: str, shape=None, dtype=torch.int32) -> None:
@@ -540,17 +544,15 @@ def _need_apart(out, **inputs) -> None:
             raise ValueError(f"out: shares memory with {name}")
 
 
-def _one_device(stream, tensors: dict) -> int:
+def _one_device(stream, first, *others) -> int:
     """The index of the CUDA device that every tensor of a call (and the
     stream) is on."""
-    dev = None
-    for t in tensors.values():
-        if t is not None:
-            d = t.get_device()
-            dev = d if dev is None else dev
-            if d != dev or d < 0:
-                where = ", ".join(f"{k} on {x.device}" for k, x in tensors.items() if x is not None)
-                raise ValueError(f"tensors must lie on one CUDA device: {where}")
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must lie on one CUDA device: {first.device} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"tensors must lie on one CUDA device: {first.device}")
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
     return dev
@@ -559,49 +561,72 @@ def _one_device(stream, tensors: dict) -> int:
 # The current stream's handle without building a Stream object (a tenth of the
 # time of torch.cuda.current_stream), where this PyTorch has the call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = torch.cuda.current_device
 
 
-def _launch(dev: int, stream, where: str, fn, *args) -> None:
-    """fn(*args, stream handle) with `dev` as the current device."""
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            return _launch(dev, stream, where, fn, *args)
+def _handle(dev: int, stream) -> int:
     if stream is not None:
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
-        handle = _raw_stream(dev)
-    else:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    status = fn(*args, handle)
-    if status != H3KV_OK:
-        raise H3kvError(status, where)
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _new(stream, shape, dtype, dev: int) -> torch.Tensor:
-    """A tensor of a call, allocated on the call's stream (see _on)."""
+def _on_device(dev: int, call, *args, **kw):
+    """The call again with `dev` as the current device."""
+    with torch.cuda.device(dev):
+        return call(*args, **kw)
+
+
+def _new_rows(stream, like: torch.Tensor, heads: int, rows: int) -> tuple[torch.Tensor, h3kv_rows]:
+    """A bf16 [heads, rows, 128] result, allocated on the call's stream (see
+    _on), and its C struct."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        out = like.new_empty((heads, rows, HEAD_DIM), dtype=torch.bfloat16)
+    else:
+        with torch.cuda.stream(stream):
+            out = like.new_empty((heads, rows, HEAD_DIM), dtype=torch.bfloat16)
+    return out, h3kv_rows(out.data_ptr(), rows * HEAD_DIM if heads > 1 else 0, HEAD_DIM if rows > 1 else 0)
+
+
+def _new(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace_bytes(q_heads: int, kv_heads: int, nodes: int, seqs: int) -> int:
+    return max(h3kv_attend_tree_workspace_bytes(q_heads, kv_heads, nodes, seqs), 32)
 
 
 class PagedStore:
     """A kvi8r cache in pages, held in torch tensors: int8 codes [pages,
     kv_heads, page_size, 128] and fp16 scales [pages, kv_heads, page_size]
     for K and for V.  Pool row r is slot r % page_size of page
-    r // page_size."""
+    r // page_size.  The four buffers are checked once and stay the same."""
+
+    __slots__ = ("_buffers", "_struct", "_ref", "pages", "kv_heads", "page_size")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
         _need(k_codes, "k_codes", torch.int8)
         if k_codes.dim() != 4 or k_codes.shape[3] != HEAD_DIM:
             raise ValueError(f"k_codes: shape {tuple(k_codes.shape)}, expected [pages, kv_heads, page_size, {HEAD_DIM}]")
-        self.k_codes, self.v_codes = k_codes, v_codes
-        self.k_scales, self.v_scales = k_scales, v_scales
-        self.pages, self.kv_heads, self.page_size = (int(x) for x in k_codes.shape[:3])
+        shape = self.pages, self.kv_heads, self.page_size = tuple(int(x) for x in k_codes.shape[:3])
         if self.page_size not in PAGE_SIZES:
             raise ValueError(f"page_size {self.page_size}, expected one of {PAGE_SIZES}")
-        self._checked = None
-        self.c_struct()
+        _need(v_codes, "v_codes", torch.int8, (*shape, HEAD_DIM))
+        _need(k_scales, "k_scales", torch.float16, shape)
+        _need(v_scales, "v_scales", torch.float16, shape)
+        self._buffers = (k_codes, v_codes, k_scales, v_scales)
+        if len({t.device for t in self._buffers}) != 1:
+            raise ValueError("the four buffers must lie on one device")
+        self._struct = h3kv_paged_store(*(t.data_ptr() for t in self._buffers), *shape, HEAD_DIM)
+        self._ref = ctypes.byref(self._struct)
+
+    k_codes = property(lambda self: self._buffers[0])
+    v_codes = property(lambda self: self._buffers[1])
+    k_scales = property(lambda self: self._buffers[2])
+    v_scales = property(lambda self: self._buffers[3])
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, page_size: int = 64, device="cuda") -> "PagedStore":
@@ -612,25 +637,7 @@ class PagedStore:
         return cls(kc, vc, ks, vs)
 
     def tensors(self) -> dict:
-        return {"store.k_codes": self.k_codes, "store.v_codes": self.v_codes, "store.k_scales": self.k_scales,
-                "store.v_scales": self.v_scales}
-
-    def c_struct(self) -> h3kv_paged_store:
-        """The C struct of the four buffers, checked again whenever one of
-        them is another than at the last call."""
-        ptrs = (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(), self.v_scales.data_ptr())
-        buffers = (self.k_codes, self.v_codes, self.k_scales, self.v_scales)
-        if self._checked is not None and self._checked[0] == ptrs and all(
-                x is y for x, y in zip(self._checked[1], buffers)):
-            return self._checked[2]
-        shape = (self.pages, self.kv_heads, self.page_size)
-        _need(self.k_codes, "store.k_codes", torch.int8, (*shape, HEAD_DIM))
-        _need(self.v_codes, "store.v_codes", torch.int8, (*shape, HEAD_DIM))
-        _need(self.k_scales, "store.k_scales", torch.float16, shape)
-        _need(self.v_scales, "store.v_scales", torch.float16, shape)
-        st = h3kv_paged_store(*ptrs, *shape, HEAD_DIM)
-        self._checked = (ptrs, buffers, st)
-        return st
+        return dict(zip(("k_codes", "v_codes", "k_scales", "v_scales"), self._buffers))
 
     def nbytes(self) -> int:
         return int(h3kv_paged_store_bytes(self.pages, self.kv_heads, self.page_size, HEAD_DIM))
@@ -644,10 +651,11 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, store: PagedStore, rows: torc
     n = K.shape[1]
     v = _need_strided(V, "V", store.kv_heads, n)
     _need_index(rows, "rows", (n,))
-    st = store.c_struct()
-    dev = _one_device(stream, {"K": K, "V": V, "rows": rows, **store.tensors()})
-    _launch(dev, stream, "h3kv_paged_append", h3kv_paged_append, ctypes.byref(k), ctypes.byref(v), rows.data_ptr(), n,
-            ctypes.byref(st))
+    dev = _one_device(stream, K, V, rows, store._buffers[0])
+    if _current_device() != dev:
+        return _on_device(dev, paged_append, K, V, store, rows, stream)
+    check(h3kv_paged_append(ctypes.byref(k), ctypes.byref(v), rows.data_ptr(), n, store._ref, _handle(dev, stream)),
+          "h3kv_paged_append")
 
 
 def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = None, V: torch.Tensor | None = None,
@@ -658,18 +666,23 @@ def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = N
     if rows.dim() != 1:
         raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [n]")
     n = rows.shape[0]
-    st = store.c_struct()
-    dev = _one_device(stream, {"rows": rows, "K": K, "V": V, **store.tensors()})
-    given = {"K": K, "V": V}
-    K = _new(stream, (store.kv_heads, n, HEAD_DIM), torch.bfloat16, dev) if K is None else K
-    V = _new(stream, (store.kv_heads, n, HEAD_DIM), torch.bfloat16, dev) if V is None else V
-    k, v = _need_strided(K, "K", store.kv_heads, n), _need_strided(V, "V", store.kv_heads, n)
-    for t in given.values():
-        _need_apart(t, rows=rows, **store.tensors())
-    if given["K"] is not None and given["V"] is not None and k.data == v.data and n and store.kv_heads:
+    dev = _one_device(stream, rows, K, V, store._buffers[0])
+    if _current_device() != dev:
+        return _on_device(dev, paged_read, store, rows, K, V, stream)
+    if K is None:
+        K, k = _new_rows(stream, rows, store.kv_heads, n)
+    else:
+        k = _need_strided(K, "K", store.kv_heads, n)
+        _need_apart(K, rows=rows, **store.tensors())
+    if V is None:
+        V, v = _new_rows(stream, rows, store.kv_heads, n)
+    else:
+        v = _need_strided(V, "V", store.kv_heads, n)
+        _need_apart(V, rows=rows, **store.tensors())
+    if k.data == v.data and n and store.kv_heads:
         raise ValueError("out: K shares memory with V")
-    _launch(dev, stream, "h3kv_paged_read", h3kv_paged_read, ctypes.byref(st), rows.data_ptr(), n, ctypes.byref(k),
-            ctypes.byref(v))
+    check(h3kv_paged_read(store._ref, rows.data_ptr(), n, ctypes.byref(k), ctypes.byref(v), _handle(dev, stream)),
+          "h3kv_paged_read")
     return K, V
 
 
@@ -681,17 +694,19 @@ def paged_copy(store: PagedStore, src: torch.Tensor, dst: torch.Tensor, stream=N
     if src.dim() != 1:
         raise ValueError(f"src: shape {tuple(src.shape)}, expected [n]")
     _need_index(dst, "dst", src.shape)
-    st = store.c_struct()
-    dev = _one_device(stream, {"src": src, "dst": dst, **store.tensors()})
-    _launch(dev, stream, "h3kv_paged_copy", h3kv_paged_copy, ctypes.byref(st), src.data_ptr(), dst.data_ptr(),
-            src.shape[0])
+    dev = _one_device(stream, src, dst, store._buffers[0])
+    if _current_device() != dev:
+        return _on_device(dev, paged_copy, store, src, dst, stream)
+    check(h3kv_paged_copy(store._ref, src.data_ptr(), dst.data_ptr(), src.shape[0], _handle(dev, stream)),
+          "h3kv_paged_copy")
 
 
 def _need_table(page_table, lengths, cu_nodes) -> int:
     _need_index(cu_nodes, "cu_nodes")
-    if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
-        raise ValueError(f"cu_nodes: shape {tuple(cu_nodes.shape)}, expected [seqs + 1]")
-    seqs = cu_nodes.shape[0] - 1
+    shape = cu_nodes.shape
+    if len(shape) != 1 or shape[0] < 1:
+        raise ValueError(f"cu_nodes: shape {tuple(shape)}, expected [seqs + 1]")
+    seqs = shape[0] - 1
     _need_index(lengths, "lengths", (seqs,))
     _need_index(page_table, "page_table")
     if page_table.dim() != 2 or page_table.shape[0] != seqs:
@@ -710,17 +725,17 @@ def paged_keep(store: PagedStore, page_table: torch.Tensor, lengths: torch.Tenso
         _need_index(keep, "keep", dtype=torch.uint8)
     if keep.dim() != 1 or not keep.is_contiguous():
         raise ValueError(f"keep: shape {tuple(keep.shape)}, expected contiguous [nodes]")
-    st = store.c_struct()
-    dev = _one_device(stream, {"page_table": page_table, "lengths": lengths, "cu_nodes": cu_nodes, "keep": keep,
-                               "out": out, **store.tensors()})
+    dev = _one_device(stream, page_table, lengths, cu_nodes, keep, out, store._buffers[0])
+    if _current_device() != dev:
+        return _on_device(dev, paged_keep, store, page_table, lengths, cu_nodes, keep, out, stream)
     if out is None:
-        out = _new(stream, (seqs,), torch.int32, dev)
+        out = _new(stream, lengths, (seqs,), torch.int32)
     else:
         _need_index(out, "out", (seqs,))
         _need_apart(out, lengths=lengths, cu_nodes=cu_nodes, page_table=page_table, keep=keep)
-    _launch(dev, stream, "h3kv_paged_keep", h3kv_paged_keep, ctypes.byref(st), page_table.data_ptr(),
-            page_table.shape[1], lengths.data_ptr(), cu_nodes.data_ptr(), seqs, keep.data_ptr(), keep.shape[0],
-            out.data_ptr())
+    check(h3kv_paged_keep(store._ref, page_table.data_ptr(), page_table.shape[1], lengths.data_ptr(),
+                          cu_nodes.data_ptr(), seqs, keep.data_ptr(), keep.shape[0], out.data_ptr(),
+                          _handle(dev, stream)), "h3kv_paged_keep")
     return out
 
 
@@ -745,22 +760,23 @@ def attend_tree(Q: torch.Tensor, store: PagedStore, page_table: torch.Tensor, le
         _need_index(parents, "parents", (nodes,))
     if lse is not None:
         _need_index(lse, "lse", (heads, nodes), torch.float32)
-    st = store.c_struct()
-    dev = _one_device(stream, {"Q": Q, "page_table": page_table, "lengths": lengths, "cu_nodes": cu_nodes,
-                               "parents": parents, "out": out, "lse": lse, "workspace": workspace, **store.tensors()})
-    given = out is not None
-    out = out if given else _new(stream, (heads, nodes, HEAD_DIM), torch.bfloat16, dev)
-    o = _need_strided(out, "out", heads, nodes)
+    dev = _one_device(stream, Q, page_table, lengths, cu_nodes, parents, out, lse, workspace, store._buffers[0])
+    if _current_device() != dev:
+        return _on_device(dev, attend_tree, Q, store, page_table, lengths, cu_nodes, parents, softmax_scale, out, lse,
+                          workspace, stream)
     if workspace is None:
-        need = h3kv_attend_tree_workspace_bytes(heads, store.kv_heads, nodes, seqs)
-        workspace = _new(stream, (max(need, 16),), torch.uint8, dev)
+        workspace = _new(stream, Q, (_tree_workspace_bytes(heads, store.kv_heads, nodes, seqs),), torch.uint8)
     else:
         _need_index(workspace, "workspace", dtype=torch.uint8)
-    if given:
+    if out is None:
+        out, o = _new_rows(stream, Q, heads, nodes)
+    else:
+        o = _need_strided(out, "out", heads, nodes)
         _need_apart(out, Q=Q, lse=lse, workspace=workspace)
-    _launch(dev, stream, "h3kv_attend_tree", h3kv_attend_tree, ctypes.byref(q), heads, nodes, ctypes.byref(st),
-            page_table.data_ptr(), page_table.shape[1], lengths.data_ptr(), cu_nodes.data_ptr(), seqs, _ptr(parents),
-            softmax_scale, ctypes.byref(o), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    check(h3kv_attend_tree(ctypes.byref(q), heads, nodes, store._ref, page_table.data_ptr(), page_table.shape[1],
+                           lengths.data_ptr(), cu_nodes.data_ptr(), seqs, 0 if parents is None else parents.data_ptr(),
+                           softmax_scale, ctypes.byref(o), 0 if lse is None else lse.data_ptr(),
+                           workspace.data_ptr(), workspace.numel(), _handle(dev, stream)), "h3kv_attend_tree")
     return out
 
 
@@ -779,21 +795,27 @@ def attend_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch
     if kv_heads < 1 or heads % kv_heads != 0:
         raise ValueError(f"Q: {heads} heads, not a multiple of K's {kv_heads}")
     _need_index(cu_q, "cu_q")
-    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        raise ValueError(f"cu_q: shape {tuple(cu_q.shape)}, expected [seqs + 1]")
-    cu_k = cu_q if cu_k is None else cu_k
-    _need_index(cu_k, "cu_k", cu_q.shape)
+    shape = cu_q.shape
+    if len(shape) != 1 or shape[0] < 1:
+        raise ValueError(f"cu_q: shape {tuple(shape)}, expected [seqs + 1]")
+    if cu_k is None:
+        cu_k = cu_q
+    else:
+        _need_index(cu_k, "cu_k", shape)
     if lse is not None:
         _need_index(lse, "lse", (heads, rows), torch.float32)
-    dev = _one_device(stream, {"Q": Q, "K": K, "V": V, "cu_q": cu_q, "cu_k": cu_k, "out": out, "lse": lse})
-    given = out is not None
-    out = out if given else _new(stream, (heads, rows, HEAD_DIM), torch.bfloat16, dev)
-    o = _need_strided(out, "out", heads, rows)
-    if given:
+    dev = _one_device(stream, Q, K, V, cu_q, cu_k, out, lse)
+    if _current_device() != dev:
+        return _on_device(dev, attend_prompt, Q, K, V, cu_q, cu_k, causal, softmax_scale, out, lse, stream)
+    if out is None:
+        out, o = _new_rows(stream, Q, heads, rows)
+    else:
+        o = _need_strided(out, "out", heads, rows)
         _need_apart(out, Q=Q, K=K, V=V, lse=lse)
-    _launch(dev, stream, "h3kv_attend_prompt", h3kv_attend_prompt, ctypes.byref(q), heads, rows, ctypes.byref(k),
-            ctypes.byref(v), kv_heads, k_rows, cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, bool(causal),
-            softmax_scale, ctypes.byref(o), _ptr(lse))
+    check(h3kv_attend_prompt(ctypes.byref(q), heads, rows, ctypes.byref(k), ctypes.byref(v), kv_heads, k_rows,
+                             cu_q.data_ptr(), cu_k.data_ptr(), shape[0] - 1, bool(causal), softmax_scale,
+                             ctypes.byref(o), 0 if lse is None else lse.data_ptr(), _handle(dev, stream)),
+          "h3kv_attend_prompt")
     return out
 
 

@@ -385,16 +385,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<PromptSegs::kDepth> r;
       uint32_t block = blockIdx.x, phase = 0, copies_phase = 0;
       bool more = true;
+      auto next_block = [&] {
+        if (lane == 0) request_block(smem_u32(sm.taken), smem_u32(&sm.taken_bar));
+        const bool came = warp_wait(smem_u32(&sm.taken_bar), phase, w);
+        // (the answer must have landed before the CTA exits)
+        if (!came) mbar_wait_drain(smem_u32(&sm.taken_bar), phase, kDrainNs);
+        phase ^= 1u;
+        const bool got = came && read_block(smem_u32(sm.taken), &block);
+        // it has been read before the next one is written over it
+        fence_proxy_async_smem();
+        __syncwarp();
+        return got;
+      };
       for (;;) {
         Seg s;
         bool found = false;
         while (more && !(found = f.find(a, tile_rows, block, &s))) {
-          // (a block that no sequence needs)
-          if (lane == 0) request_block(smem_u32(sm.taken), smem_u32(&sm.taken_bar));
-          more = warp_wait(smem_u32(&sm.taken_bar), phase, w) && read_block(smem_u32(sm.taken), &block);
-          phase ^= 1u;
-          fence_proxy_async_smem();
-          __syncwarp();
+          more = next_block();  // (a block that no sequence needs)
         }
         if (!found) s.rows = s.n = 0;
         if (!warp_wait(smem_u32(&sm.segs.empty[r.slot]), r.phase ^ 1u, w)) break;
@@ -410,12 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // here while other SMs run out of work
         if (!warp_wait(smem_u32(&sm.last_copies), copies_phase, w)) break;
         copies_phase ^= 1u;
-        if (lane == 0) request_block(smem_u32(sm.taken), smem_u32(&sm.taken_bar));
-        more = warp_wait(smem_u32(&sm.taken_bar), phase, w) && read_block(smem_u32(sm.taken), &block);
-        phase ^= 1u;
-        // the answer has been read before the next one is written over it
-        fence_proxy_async_smem();
-        __syncwarp();
+        more = next_block();
       }
     }
   }
@@ -438,7 +440,8 @@ cudaError_t launch_attend_prompt(const PromptArgs &a, cudaStream_t stream) {
                       static_cast<uintptr_t>(a.o.row_stride * 2)) &
                      31) == 0;
   auto kernel = wide ? prompt_kernel<true> : prompt_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmemBytes);
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t e = allow_smem(kernel, kPromptSmemBytes, allowed[wide]);
   if (e != cudaSuccess) return e;
   // every sequence may end in a part of a row tile
   auto units = [&](int64_t rows) { return ((a.q_rows + rows - 1) / rows + a.seqs) * a.q_heads; };

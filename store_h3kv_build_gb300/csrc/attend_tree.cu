@@ -453,7 +453,8 @@ cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
                         static_cast<uintptr_t>(a.o.row_stride * 2)) &
                        31) == 0;
     auto kernel = wide ? tree_kernel<true> : tree_kernel<false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTreeSmemBytes));
+    static std::atomic<uint64_t> allowed[2];
+    e = allow_smem(kernel, static_cast<int>(kTreeSmemBytes), allowed[wide]);
     if (e != cudaSuccess) return e;
     kernel<<<a.ctas, kThreads, kTreeSmemBytes, stream>>>(a);
     e = cudaGetLastError();

@@ -437,7 +437,8 @@ template <int kNT>
 cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a, cudaStream_t stream) {
   constexpr int kBytes = sizeof(FewSmem<kNT>) + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
-  const cudaError_t e = cudaFuncSetAttribute(few_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t e = allow_smem(few_kernel<kNT>, kBytes, allowed);
   if (e != cudaSuccess) return e;
   few_kernel<kNT><<<a.ctas, kFewThreads, kBytes, stream>>>(tk, tv, a);
   return cudaGetLastError();

@@ -397,7 +397,8 @@ cudaError_t launch_paged_append(const PagedArgs &p, const h3kv_rows &K, const h3
   // whole 32-byte sectors per store where the codes' alignment allows
   const bool wide = ((reinterpret_cast<uintptr_t>(p.k_codes) | reinterpret_cast<uintptr_t>(p.v_codes)) & 31) == 0;
   auto kernel = wide ? append_kernel<true> : append_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmemBytes);
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t e = allow_smem(kernel, kAppendSmemBytes, allowed[wide]);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (n + kTokens - 1) / kTokens * p.kv_heads * 2;
   const unsigned grid = static_cast<unsigned>(tiles < 2 * d.num_sms ? tiles : 2 * d.num_sms);

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/h3kv_serve.h"
 
 namespace h3kv {
@@ -26,6 +28,20 @@ h3kv_status serve_device(ServeDevice *out);
 // 3-D map over strided bf16 [heads, rows, 128]: box 64 columns x box_rows rows
 // x 1 head, 128-byte swizzle; rows past `rows` read as zero (abi.cu).
 bool encode_rows_bf16(CUtensorMap *m, const h3kv_rows &r, int64_t heads, int64_t rows, uint32_t box_rows);
+
+// Allows `kernel` its dynamic shared memory, once per device (`done`: a bit for
+// each of the 64 devices the library knows).
+template <class Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct PagedArgs {
   int8_t *k_codes, *v_codes;

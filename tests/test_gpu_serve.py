@@ -149,6 +149,84 @@ def test_prompt_values_of_other_sequences_do_not_reach(cuda):
             assert torch.equal(out[:, a0:a1], ref[:, a0:a1])
 
 
+def shifted(shape, dtype=torch.bfloat16, fill=7.0, by=16):
+    """A tensor that starts `by` bytes behind a 512-byte boundary."""
+    n, off = int(np.prod(shape)), by // torch.empty((), dtype=dtype).element_size()
+    return torch.full((n + off,), fill, dtype=dtype, device=DEV)[off:].view(shape)
+
+
+def test_sixteen_byte_alignment_is_enough(cuda):
+    # outputs and pools 16 bytes off give the bits of aligned ones (their
+    # kernels write 32 bytes at a time)
+    n = [130, 70, 300]
+    q, k, v = (normal(s, 2, 500, 128) for s in (1, 2, 3))
+    cu = i32(cu_of(n))
+    ref = b.attend_prompt(q.to(DEV), k.to(DEV), v.to(DEV), cu)
+    off = [shifted(x.shape).copy_(x.to(DEV)) for x in (q, k, v)]
+    assert torch.equal(b.attend_prompt(*off, cu, out=shifted(q.shape)), ref)
+    tok = shifted((500, 2, 128)).transpose(0, 1)
+    assert torch.equal(b.attend_prompt(*off, cu, out=tok), ref)
+    st, _ = random_store(6, 2, 64)
+    st2 = b.PagedStore(*(shifted(t.shape, t.dtype, 0).copy_(t) for t in st.tensors().values()))
+    rows = i32(torch.randperm(384)[:140].tolist())
+    for s in (st, st2):
+        b.paged_append(k[:, :140].contiguous().to(DEV), v[:, :140].contiguous().to(DEV), s, rows)
+    for x, y in zip(st.tensors().values(), st2.tensors().values()):
+        assert torch.equal(x, y)
+    a = b.paged_read(st, rows)
+    c = b.paged_read(st2, rows, shifted((2, 140, 128)), shifted((140, 2, 128)).transpose(0, 1))
+    assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])
+    for nodes, hq in ((2, 4), (8, 4), (64, 8)):
+        qq = normal(9, hq, nodes, 128).to(DEV)
+        args = i32_2d([[4, 0, 5, 2, 1, 3]]), i32([380]), i32([0, nodes])
+        assert torch.equal(b.attend_tree(qq, st, *args), b.attend_tree(qq, st2, *args, out=shifted(qq.shape)))
+    b.paged_copy(st, i32([0, 1]), i32([3, 4]))
+    b.paged_copy(st2, i32([0, 1]), i32([3, 4]))
+    for x, y in zip(st.tensors().values(), st2.tensors().values()):
+        assert torch.equal(x, y)
+    b.sync_status()
+
+
+def test_offsets_beyond_31_bits(cuda):
+    # the last pages of a pool of 4.3 GB of codes for K (and for V), the last
+    # rows of prompts of 4.5 GB
+    pages, hk, ps = 1 << 15, 8, 128
+    st = b.PagedStore.empty(pages, hk, ps)
+    k, v = normal(1, hk, 300, 128), normal(2, hk, 300, 128)
+    table = [pages - 1, pages - 3, 0]
+    rows = [table[p // ps] * ps + p % ps for p in range(300)]
+    b.paged_append(k.to(DEV), v.to(DEV), st, i32(rows))
+    b.paged_copy(st, i32([0]), i32([pages - 2]))
+    table[2] = pages - 2
+    rk, rv = b.paged_read(st, i32([table[p // ps] * ps + p % ps for p in range(300)]))
+    part = {n: t[[pages - 1, pages - 3, pages - 2]].cpu() for n, t in st.tensors().items()}
+    ref = {n: t.double().numpy() if "scales" in n else t.numpy() for n, t in part.items()}
+    for x, back in ((k, rk), (v, rv)):
+        codes, scales = oracle.encode_rows(x)
+        off = 1.1 * scales[..., None] + 2.0 ** -8 * np.abs(oracle.as_f64(back)) + 1e-6
+        within(back, oracle.unrotate(oracle.dequant(codes, scales)), off, "read")
+    for hq, nodes in ((8, 1), (16, 7), (32, 60)):
+        q = normal(3, hq, nodes, 128)
+        out = b.attend_tree(q.to(DEV), st, i32_2d([table]), i32([300]), i32([0, nodes]))
+        want = so.attend_tree(q, ref, [[0, 1, 2]], [300], [0, nodes])
+        within(out, want[0], want[2], f"tree {nodes}")
+    cu, keep = i32([0, 60]), torch.zeros(60, dtype=torch.uint8, device=DEV)
+    keep[40:] = 1
+    assert b.paged_keep(st, i32_2d([table]), i32([300]), cu, keep).tolist() == [260]
+    moved = st.k_codes[table[2], :, :4].cpu()
+    assert torch.equal(moved, part["k_codes"][2, :, 40:44])  # tokens 256 .. 259 were nodes 56 .. 59, tokens 296 .. 299
+    del st
+    n = (1 << 21) + 1000
+    q, k, v = (torch.zeros((8, n, 128), dtype=torch.bfloat16, device=DEV) for _ in range(3))
+    parts = [normal(s, 8, 400, 128) for s in (4, 5, 6)]
+    for t, x in zip((q, k, v), parts):
+        t[:, n - 400:] = x.to(DEV)
+    out = b.attend_prompt(q, k, v, i32([n - 400, n - 130, n]))
+    b.sync_status()
+    want = so.attend_prompt(*parts, [0, 270, 400], [0, 270, 400])
+    within(out[:, n - 400:], want[0], want[2], "prompt")
+
+
 def test_prompt_same_bits_wherever_a_sequence_lies(cuda):
     q, k, v = (normal(s, 2, 900, 128).to(DEV) for s in (1, 2, 3))
     alone = b.attend_prompt(q[:, 137:600].contiguous(), k[:, 137:600].contiguous(), v[:, 137:600].contiguous(),
@@ -422,6 +500,13 @@ def test_tree_many_sequences(cuda):
     tree_case(lens, nodes, 2, 1, 16, seed=6)
 
 
+def test_tree_many_sequences_of_many_rows(cuda):
+    g = np.random.default_rng(5)
+    lens = g.integers(10, 120, 620).tolist()
+    nodes = [int(g.integers(5, min(n, 14) + 1)) for n in lens]
+    tree_case(lens, nodes, 4, 1, 16, seed=6)
+
+
 def test_tree_long_cache(cuda):
     tree_case([30000], [4], 4, 1, 64, seed=7)
     tree_case([9000, 11000], [1, 64], 8, 1, 128, seed=8)
@@ -644,6 +729,59 @@ def test_serving_step_replays_from_a_graph(cuda):
         assert torch.equal(got[0], out) and torch.equal(got[1], left)
         for x, y in zip(st.tensors().values(), st2.tensors().values()):
             assert torch.equal(x, y)
+
+
+def test_prompt_replays_from_a_graph(cuda):
+    q, k, v = normal(1, 40, 900, 128).to(DEV), normal(2, 4, 900, 128).to(DEV), normal(3, 4, 900, 128).to(DEV)
+    cu, out = i32([0, 300, 900]), torch.zeros_like(q)
+    b.attend_prompt(q, k, v, cu, out=out)
+    b.sync_status()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.attend_prompt(q, k, v, cu, out=out)
+    for seed, c in ((4, [0, 300, 900]), (5, [0, 899, 900]), (6, [10, 11, 500])):
+        q.copy_(normal(seed, 40, 900, 128))
+        cu.copy_(i32(c))
+        g.replay()
+        b.sync_status()
+        got = out.clone()
+        assert torch.equal(b.attend_prompt(q, k, v, cu)[:, c[0]:c[2]], got[:, c[0]:c[2]])
+
+
+def test_withheld_arrivals_run_into_the_wait_limit(cuda):
+    """Each attention kernel of the serving operators with one arrival left
+    out: its bounded wait runs out, the status says so, and the context and
+    the next call are sound."""
+    st, _ = random_store(40, 8, 128)
+    t = i32_2d([list(range(40))])
+    q = normal(1, 8, 1500, 128).to(DEV)
+    qt = {n: normal(2, 64, n, 128).to(DEV) for n in (1, 2, 40)}
+    calls = [lambda: b.attend_prompt(q, q, q, i32([0, 1500])),
+             lambda: b.attend_tree(qt[40], st, t, i32([5000]), i32([0, 40]))]
+    # the kernels for few rows wait for a freed stage, which takes more tiles
+    # than stages on a CTA: many sequences over the same pages
+    many = 24
+    for n in (1, 2):
+        qm = qt[n].repeat(1, many, 1)
+        calls.append(lambda qm=qm, n=n: b.attend_tree(qm, st, t.expand(many, 40).contiguous(), i32([5000] * many),
+                                                      i32(range(0, many * n + 1, n))))
+    try:
+        for call in calls:
+            want = call()
+            b.sync_status()
+            assert b.h3kv_set_wait_timeout_ns(2_000_000) == b.H3KV_OK
+            assert b.h3kv_debug_withhold_p(1) == b.H3KV_OK
+            call()
+            with pytest.raises(b.H3kvError) as e:
+                b.sync_status()
+            assert e.value.status == b.H3KV_ERR_DEVICE_TIMEOUT
+            assert b.h3kv_debug_withhold_p(-1) == b.H3KV_OK
+            assert b.h3kv_set_wait_timeout_ns(0) == b.H3KV_OK
+            assert torch.equal(call(), want)
+            b.sync_status()
+    finally:
+        b.h3kv_debug_withhold_p(-1)
+        b.h3kv_set_wait_timeout_ns(0)
 
 
 def test_calls_on_two_streams_at_once(cuda):
