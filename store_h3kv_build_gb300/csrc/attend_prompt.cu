@@ -167,15 +167,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_base + q * 128, tO = tmem + lane_base + 256 + q * 128;
     const float c2 = a.scale_log2;
     const int i = tid & 127;  // row in the tile == TMEM lane
-    uint32_t phase = 0, o_phase = 0;
-    for (;;) {
-      // the eight warps go on, or leave, together
-      if (!named_bar_and(1, 256, sr.get(sm.segs, w))) break;
+    uint32_t phase = 0;
+    StreamEnd fin;
+    while (sr.get(sm.segs, w)) {
       const Seg &s = sr.seg(sm.segs);
       if (s.rows == 0) break;
       const int r = (s.two ? q * kBM : 0) + i;  // row in the segment
       const bool warp_on = (s.two ? q * kBM : 0) + (warp & 3) * 32 < s.rows;
-      const int n_tiles = s.n;
       // keys u < see_keys are seen by this row
       int32_t see_keys;
       {
@@ -208,62 +206,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
         if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.p_full[q]));
       }
-      const bool two = s.two;
-      if (n_tiles > 0) {
-        ok = ok && warp_wait(smem_u32(&sm.o_full), o_phase, w);
-        o_phase ^= 1u;
-      }
-      tc_fence_after();
-      // stream 1's maxima and sums for the join; both warpgroups leave together
-      if (!two && q == 1) sm.ml[i] = make_float2(row.m, row.l);
-      if (!named_bar_and(1, 256, ok)) break;
-      if (two || q == 0) {
-        const bool joined = !two && n_tiles > 1, any = t_first < end;
-        float ga = 1.f, gb = 0.f;
-        if (joined) join_rows(row, sm.ml[i], c2, ga, gb);
+      bool joined;
+      float ga, gb;
+      const End e = ok ? fin.at_end(sm, s, q, warp_on, row, c2, &joined, &ga, &gb, w) : kFailed;
+      if (e == kFailed) break;
+      if (e == kWrite) {
+        const bool any = t_first < end;
         const bool none = row.l == 0.f;  // the row sees no key
         const float inv = none ? 0.f : 1.f / row.l;
-        if (warp_on) {
-          const int64_t at = s.q_base + s.row0 + r;
-          uint16_t *dst = a.o.data + s.head * a.o.head_stride + at * a.o.row_stride;
-          const bool live = r < s.rows;
-          // a thread writes its row, 32 bytes at a time where the alignment
-          // allows; a loop, since instructions that run once a segment are
-          // waited for
-          const float gx = ga * inv, gy = gb * inv;
+        const int64_t at = s.q_base + s.row0 + r;
+        uint16_t *dst = a.o.data + s.head * a.o.head_stride + at * a.o.row_stride;
+        const bool live = r < s.rows;
+        // a thread writes its row, 32 bytes at a time where the alignment
+        // allows; a loop, since instructions that run once a segment are
+        // waited for
+        const float gx = ga * inv, gy = gb * inv;
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            float x[16];
-            if (any) {
-              tmem_ld16(tO + c * 16, *reinterpret_cast<uint32_t(*)[16]>(x));
+        for (int c = 0; c < 8; ++c) {
+          float x[16];
+          if (any) {
+            tmem_ld16(tO + c * 16, *reinterpret_cast<uint32_t(*)[16]>(x));
 #pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] *= gx;
-              if (joined) {
-                float y[16];
-                tmem_ld16(tO + 128 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(y));
+            for (int k = 0; k < 16; ++k) x[k] *= gx;
+            if (joined) {
+              float y[16];
+              tmem_ld16(tO + 128 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(y));
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = fmaf(y[k], gy, x[k]);
-              }
-            }
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = none ? 0u : pack_bf16x2(x[2 * k], x[2 * k + 1]);
-            if (live) {
-              if constexpr (kWide) {
-                st_global_v8(dst + 16 * c, h);
-              } else {
-                reinterpret_cast<uint4 *>(dst)[2 * c] = make_uint4(h[0], h[1], h[2], h[3]);
-                reinterpret_cast<uint4 *>(dst)[2 * c + 1] = make_uint4(h[4], h[5], h[6], h[7]);
-              }
+              for (int k = 0; k < 16; ++k) x[k] = fmaf(y[k], gy, x[k]);
             }
           }
-          if (a.lse && live)
-            a.lse[s.head * a.q_rows + at] = none ? -INFINITY : kLn2 * (row.m * c2 + log2f(row.l));
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = none ? 0u : pack_bf16x2(x[2 * k], x[2 * k + 1]);
+          if (live) {
+            if constexpr (kWide) {
+              st_global_v8(dst + 16 * c, h);
+            } else {
+              reinterpret_cast<uint4 *>(dst)[2 * c] = make_uint4(h[0], h[1], h[2], h[3]);
+              reinterpret_cast<uint4 *>(dst)[2 * c + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          }
         }
+        if (a.lse && live)
+          a.lse[s.head * a.q_rows + at] = none ? -INFINITY : kLn2 * (row.m * c2 + log2f(row.l));
       }
-      // stream 1's O and (max, sum) have been read
-      if (!two) named_bar_sync(2, 256);
-      tc_fence_before();
+      fin.read_done(sm, joined);
       sr.done(sm.segs);
     }
   } else if (warp < 12) {

@@ -141,11 +141,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     const uint32_t tS = tmem + lane_base + q * 128, tO = tmem + lane_base + 256 + q * 128;
     const float c2 = a.scale_log2;
     const int i = tid & 127;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0;
     bool first = true;
-    for (;;) {
-      // the eight warps go on, or leave, together
-      if (!named_bar_and(1, 256, sr.get(sm.segs, w))) break;
+    StreamEnd fin;
+    while (sr.get(sm.segs, w)) {
       const Seg &s = sr.seg(sm.segs);
       if (s.n == 0) break;
       const int base_row = s.two ? q * kBM : 0;
@@ -188,16 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
         // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
         if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.p_full[q]));
       }
-      ok = ok && warp_wait(smem_u32(&sm.o_full), o_phase, w);
-      o_phase ^= 1u;
-      tc_fence_after();
-      if (!s.two && q == 1) sm.ml[i] = make_float2(row.m, row.l);
-      ok = named_bar_and(1, 256, ok);
-      if (!ok) break;
-      if ((s.two || q == 0) && warp_on) {
-        const bool joined = !s.two && s.n > 1;
-        float ga = 1.f, gb = 0.f;
-        if (joined) join_rows(row, sm.ml[i], c2, ga, gb);
+      bool joined;
+      float ga, gb;
+      const End e = ok ? fin.at_end(sm, s, q, warp_on, row, c2, &joined, &ga, &gb, w) : kFailed;
+      if (e == kFailed) break;
+      if (e == kWrite) {
         const bool live = r < s.rows;
         if (s.whole) {
           float o[128];
@@ -244,9 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           if (live) ws.ml[at] = make_float2(row.m, row.l);
         }
       }
-      // stream 1's O and (max, sum) have been read
-      if (!s.two) named_bar_sync(2, 256);
-      tc_fence_before();
+      fin.read_done(sm, joined);
       sr.done(sm.segs);
     }
   } else if (warp < 12) {

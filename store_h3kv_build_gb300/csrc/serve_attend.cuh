@@ -60,7 +60,8 @@ struct Smem {
   uint64_t k_load[kNK], k_ready[kNK], k_free[kNK];
   uint64_t v_load[kNV], v_ready[kNV], v_free[kNV];
   uint64_t s_full[2], p_full[2];
-  uint64_t o_full, drain;
+  uint64_t o_full[2], drain;
+  uint64_t ml_full[4], ml_free[4];  // per warp: stream 1's ml are written; its O and ml have been read
   uint64_t q_free[2];        // the stream's last QK of a segment is done
   uint64_t v_tail, v_fixed;  // prompts: a ragged last V tile has come; its rest is zeroed
   uint32_t tmem_base;
@@ -141,6 +142,7 @@ __device__ __forceinline__ void init_barriers(Smem &sm, bool cache) {
   for (int q = 0; q < 2; ++q) {
     mbar_init(smem_u32(&sm.q_full[q]), cache ? 4 : 1);
     mbar_init(smem_u32(&sm.s_full[q]), 1);
+    mbar_init(smem_u32(&sm.o_full[q]), 1);
     mbar_init(smem_u32(&sm.q_free[q]), 1);
     mbar_init(smem_u32(&sm.p_full[q]), 4);
   }
@@ -154,7 +156,10 @@ __device__ __forceinline__ void init_barriers(Smem &sm, bool cache) {
     mbar_init(smem_u32(&sm.v_ready[s]), 4);
     mbar_init(smem_u32(&sm.v_free[s]), 1);
   }
-  mbar_init(smem_u32(&sm.o_full), 1);
+  for (int i = 0; i < 4; ++i) {
+    mbar_init(smem_u32(&sm.ml_full[i]), 1);
+    mbar_init(smem_u32(&sm.ml_free[i]), 1);
+  }
   mbar_init(smem_u32(&sm.drain), 1);
   mbar_init(smem_u32(&sm.v_tail), 1);
   mbar_init(smem_u32(&sm.v_fixed), 4);
@@ -259,14 +264,15 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
       issue_pv(m, q, m.v.slot, t != first_tile(s, q));
       if (!s.two || q == 1) mma_commit(m.go, smem_u32(&sm.v_free[m.v.slot]));
       const int tn = t + step;
-      if (tn < end_tile(s, q)) {
+      if (tn >= end_tile(s, q)) {
+        mma_commit(m.go, smem_u32(&sm.o_full[q]));
+      } else {
         const bool first_user = !s.two || q == 0 || tn >= s.n0;
         if (!qk(q, first_user, !s.two || q == 1, tn + step >= end_tile(s, q))) return false;
       }
     }
     m.v.next();
   }
-  mma_commit(m.go, smem_u32(&sm.o_full));
   return true;
 }
 
@@ -381,6 +387,59 @@ __device__ __forceinline__ void join_rows(Row &r, float2 other, float c2, float 
   r.l = fmaf(r.l, ga, other.y * gb);
   r.m = m;
 }
+
+// The end of a segment for a softmax warp; the warps do not wait for one
+// another.  at_end waits for the stream's O.  Where the two streams share their
+// rows, stream 1 hands its (max, sum) over and waits until its O has been read,
+// and stream 0 takes both.  kOff: nothing to write (stream 1 of shared rows, or
+// a warp without rows); kFailed: a wait ran out.
+enum End { kFailed, kOff, kWrite };
+struct StreamEnd {
+  uint32_t o_phase[2] = {0, 0};
+  uint32_t ml_phase = 0;
+  __device__ __forceinline__ End at_end(Smem &sm, const Seg &s, int q, bool warp_on, Row &row, float c2, bool *joined,
+                                        float *ga, float *gb, const WaitCtx &w) {
+    const int wi = (threadIdx.x >> 5) & 3, i = threadIdx.x & 127;
+    const bool share = !s.two && s.n > 1;
+    bool ok = true;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (!has_tiles(s, x)) continue;
+      if (x == q || (share && q == 0)) ok = ok && warp_wait(smem_u32(&sm.o_full[x]), o_phase[x], w);
+      o_phase[x] ^= 1u;
+    }
+    if (!ok) return kFailed;
+    tc_fence_after();
+    *joined = false;
+    *ga = 1.f;
+    *gb = 0.f;
+    if (!warp_on) return kOff;
+    if (s.two) return kWrite;
+    if (q == 1) {
+      if (!share) return kOff;
+      sm.ml[i] = make_float2(row.m, row.l);
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.ml_full[wi]));
+      ok = warp_wait(smem_u32(&sm.ml_free[wi]), ml_phase, w);
+      ml_phase ^= 1u;
+      tc_fence_after();
+      return ok ? kOff : kFailed;
+    }
+    if (share) {
+      if (!warp_wait(smem_u32(&sm.ml_full[wi]), ml_phase, w)) return kFailed;
+      ml_phase ^= 1u;
+      join_rows(row, sm.ml[i], c2, *ga, *gb);
+      *joined = true;
+    }
+    return kWrite;
+  }
+  // The warp has read what O it needed.
+  __device__ __forceinline__ void read_done(Smem &sm, bool joined) const {
+    tc_fence_before();
+    __syncwarp();
+    if (joined && (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.ml_free[(threadIdx.x >> 5) & 3]));
+  }
+};
 
 constexpr float kLn2 = 0.6931471805599453f;
 
