@@ -27,14 +27,42 @@ __device__ __forceinline__ int32_t row_of_token(const PagedArgs &p, const int32_
   return -1;
 }
 
+// The tiles that a CTA walks: token tile x of y = 2 head + (V ? 1 : 0), from
+// tile blockIdx.x in steps of gridDim.x.  (A 64-bit division for each tile was
+// a third of the read kernel's instructions.)
+constexpr int kTokens = 128;
+struct TileWalk {
+  int32_t x, y, tiles_x, tiles_y, dx, dy;
+  __device__ __forceinline__ TileWalk(int64_t n, int32_t kv_heads, uint32_t first, uint32_t step) {
+    tiles_x = static_cast<int32_t>((n + kTokens - 1) / kTokens);
+    tiles_y = 2 * kv_heads;
+    dx = static_cast<int32_t>(step % tiles_x);
+    dy = static_cast<int32_t>(step / tiles_x);
+    x = static_cast<int32_t>(first % tiles_x);
+    y = static_cast<int32_t>(first / tiles_x);
+  }
+  __device__ __forceinline__ bool in() const { return y < tiles_y; }
+  __device__ __forceinline__ int32_t token() const { return x * kTokens; }
+  __device__ __forceinline__ int32_t head() const { return y >> 1; }
+  __device__ __forceinline__ bool v() const { return y & 1; }
+  __device__ __forceinline__ void next() {
+    x += dx;
+    y += dy;
+    if (x >= tiles_x) {
+      x -= tiles_x;
+      ++y;
+    }
+  }
+};
+
 // ----------------------------------------------------------------- append --
 // A persistent CTA walks 128-token tiles of one head of K or of V; a producer
 // warp streams them into a ring with TMA (whatever the strides), and two
 // threads share a row.  H128 = [[H64, H64], [H64, -H64]]: thread hf forms the
 // sum (hf 0) or difference (hf 1) of the row's halves and transforms 64 values
 // in registers, so a row costs no shuffle but the one for its absmax.  (With a
-// row over 8 lanes, 48 shuffles for 4 rows, it ran at 3.5 TB/s.)
-constexpr int kTokens = 128;
+// row over 8 lanes, 48 shuffles for 4 rows, it ran at 3.5 TB/s.)  65536 rows of
+// 8 heads: 71.5 us, 5.66 TB/s; 217088: 225 us, 5.96 TB/s; bound by HBM.
 constexpr int kComputeWarps = 2 * kTokens / 32;
 constexpr int kAppendThreads = 2 * kTokens + 32;
 constexpr int kAppendStages = 3;
@@ -68,7 +96,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   AppendSmem &sm = *reinterpret_cast<AppendSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t token_tiles = (n + kTokens - 1) / kTokens, tiles = token_tiles * p.kv_heads * 2;
+  TileWalk t(n, p.kv_heads, blockIdx.x, gridDim.x);
   if (tid == 0) {
     for (int s = 0; s < kAppendStages; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
@@ -84,16 +112,14 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
   if (warp == kComputeWarps) {
     const uint32_t go = elect_one();
     int issued[kAppendStages] = {};
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const int64_t y = t / token_tiles;
-      const int32_t token = static_cast<int32_t>(t - y * token_tiles) * kTokens, head = static_cast<int32_t>(y >> 1);
+    for (; t.in(); t.next()) {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.empty[slot]), phase ^ 1u, w))) break;
       if (go) {
-        const CUtensorMap *map = (y & 1) ? &tm_v : &tm_k;
+        const CUtensorMap *map = t.v() ? &tm_v : &tm_k;
         const uint32_t bar = smem_u32(&sm.full[slot]), dst = smem_u32(sm.in[slot]);
         mbar_arrive_expect_tx(bar, kTokenTileBytes);
-        tma_load_3d(dst, map, 0, token, head, bar);
-        tma_load_3d(dst + kTokenTileBytes / 2, map, 64, token, head, bar);
+        tma_load_3d(dst, map, 0, t.token(), t.head(), bar);
+        tma_load_3d(dst + kTokenTileBytes / 2, map, 64, t.token(), t.head(), bar);
       }
       ++issued[slot];
       if (++slot == kAppendStages) {
@@ -110,10 +136,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
   }
   const int i = tid >> 1, hf = tid & 1;  // row in the tile, half of the result
   const float2 sign = hf ? make_float2(-1.f, -1.f) : make_float2(1.f, 1.f);
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t y = t / token_tiles, token = (t - y * token_tiles) * kTokens + i;
-    const int32_t head = static_cast<int32_t>(y >> 1);
-    const int32_t r = row_of_token(p, rows, token, n);
+  for (; t.in(); t.next()) {
+    const int32_t r = row_of_token(p, rows, static_cast<int64_t>(t.token()) + i, n);
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), phase, w))) return;
     // 2^-7 first (exact), so that a sum of 128 of the largest bf16 values stays
     // finite; the values that it makes subnormal lie far below the least scale
@@ -158,8 +182,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     const float sf = __half2float(s);
     const float m = sf > 0.f ? kInvSqrt128 * 128.0f / sf : 0.f;
     if (r >= 0) {
-      const int64_t at = pool_row(p, r, head);
-      uint8_t *dst = reinterpret_cast<uint8_t *>((y & 1) ? p.v_codes : p.k_codes) + at * 128 + hf * 64;
+      const int64_t at = pool_row(p, r, t.head());
+      uint8_t *dst = reinterpret_cast<uint8_t *>(t.v() ? p.v_codes : p.k_codes) + at * 128 + hf * 64;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t c[8];
@@ -175,7 +199,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
           reinterpret_cast<uint4 *>(dst)[2 * g + 1] = make_uint4(c[4], c[5], c[6], c[7]);
         }
       }
-      if (hf == 0) ((y & 1) ? p.v_scales : p.k_scales)[at] = __half_as_ushort(s);
+      if (hf == 0) (t.v() ? p.v_scales : p.k_scales)[at] = __half_as_ushort(s);
     }
   }
 }
@@ -186,27 +210,39 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
 // exchanges sums and differences (H128 = H2 x H64).  The next tile's codes, and
 // the row numbers of the one after it, are loaded before the present one is
 // worked on.
+// A warp's 16 rows leave by TMA from a buffer of its own, two of them in turn:
+// whole lines (written in 32-byte pieces from registers, 4.46 TB/s became 4.93).
+// 65536 rows of 8 heads: 75.6 us, 5.35 TB/s; 217088: 237 us, 5.65 TB/s.  Codes
+// brought by asynchronous copies, three tiles ahead, were 4 % slower: it is
+// issue slots that are short (a row takes 33 warp instructions), not loads.
+constexpr int kReadRows = 16;                       // rows of a warp in a tile
+constexpr int kReadHalfBytes = kReadRows * 128;     // 64 channels of them
+constexpr int kReadSmemBytes = kThreads / 32 * 2 * 2 * kReadHalfBytes + 1024;
+
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 2)
-    read_kernel(const PagedArgs p, const int32_t *__restrict__ rows, const int64_t n, const h3kv_rows K,
-                const h3kv_rows V) {
-  const int i = threadIdx.x >> 1, hf = threadIdx.x & 1;
-  const int64_t token_tiles = (n + kTokens - 1) / kTokens, tiles = token_tiles * p.kv_heads * 2;
+    read_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const PagedArgs p, const int32_t *__restrict__ rows, const int64_t n) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *out = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+                 (threadIdx.x >> 5) * (4 * kReadHalfBytes);
+  const int i = threadIdx.x >> 1, hf = threadIdx.x & 1, lane = threadIdx.x & 31;
+  int buf = 0;
   struct Row {
     uint4 c[4];
     uint16_t s;
   };
-  auto index = [&](int64_t t) {
-    return t < tiles ? row_of_token(p, rows, t % token_tiles * kTokens + i, n) : -1;
+  auto index = [&](const TileWalk &t) {
+    return t.in() ? row_of_token(p, rows, static_cast<int64_t>(t.token()) + i, n) : -1;
   };
-  auto load = [&](int64_t t, int32_t r) {
+  auto load = [&](const TileWalk &t, int32_t r) {
     Row x;
     x.s = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g) x.c[g] = make_uint4(0, 0, 0, 0);
     if (r >= 0) {
-      const int64_t y = t / token_tiles, at = pool_row(p, r, static_cast<int32_t>(y >> 1));
-      const uint4 *src = reinterpret_cast<const uint4 *>(((y & 1) ? p.v_codes : p.k_codes) + at * 128) + hf * 4;
+      const int64_t at = pool_row(p, r, t.head());
+      const uint4 *src = reinterpret_cast<const uint4 *>((t.v() ? p.v_codes : p.k_codes) + at * 128) + hf * 4;
       if constexpr (kWide) {
         ld_global_v8(src, x.c[0], x.c[1]);
         ld_global_v8(src + 2, x.c[2], x.c[3]);
@@ -214,16 +250,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int g = 0; g < 4; ++g) x.c[g] = src[g];
       }
-      x.s = ((y & 1) ? p.v_scales : p.k_scales)[at];
+      x.s = (t.v() ? p.v_scales : p.k_scales)[at];
     }
     return x;
   };
-  Row next = load(blockIdx.x, index(blockIdx.x));
-  int32_t r = index(static_cast<int64_t>(blockIdx.x) + gridDim.x);
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+  TileWalk t(n, p.kv_heads, blockIdx.x, gridDim.x), ahead = t;
+  Row next = load(t, index(t));
+  ahead.next();
+  int32_t r = index(ahead);
+  for (; t.in(); t.next()) {
     const Row row = next;
-    next = load(t + gridDim.x, r);
-    r = index(t + 2 * static_cast<int64_t>(gridDim.x));
+    next = load(ahead, r);
+    ahead.next();
+    r = index(ahead);
     float x[64];
     const __half s = __ushort_as_half(row.s);
 #pragma unroll
@@ -248,24 +287,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       x[e] = z.x;
       x[e + 1] = z.y;
     }
-    const int64_t y = t / token_tiles, token = (t - y * token_tiles) * kTokens + i;
-    if (token < n) {
-      const h3kv_rows &out = (y & 1) ? V : K;
-      uint4 *dst = reinterpret_cast<uint4 *>(out.data + (y >> 1) * out.head_stride + token * out.row_stride) + hf * 8;
+    // the buffer's store before last has read it
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+    uint8_t *half = out + buf * (2 * kReadHalfBytes) + hf * kReadHalfBytes;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t c[8];
+    for (int g = 0; g < 8; ++g) {
+      uint32_t c[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = pack_bf16x2(x[16 * g + 2 * k], x[16 * g + 2 * k + 1]);
-        if constexpr (kWide) {
-          st_global_v8(dst + 2 * g, c);
-        } else {
-          dst[2 * g] = make_uint4(c[0], c[1], c[2], c[3]);
-          dst[2 * g + 1] = make_uint4(c[4], c[5], c[6], c[7]);
-        }
-      }
+      for (int k = 0; k < 4; ++k) c[k] = pack_bf16x2(x[8 * g + 2 * k], x[8 * g + 2 * k + 1]);
+      *reinterpret_cast<uint4 *>(half + sw128_off(lane >> 1, g)) = make_uint4(c[0], c[1], c[2], c[3]);
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    const int32_t token = t.token() + (i & ~(kReadRows - 1));
+    if (lane == 0) {
+      if (token < n) {  // (rows from n on are not written: they lie outside the map)
+        const CUtensorMap *map = t.v() ? &tm_v : &tm_k;
+        const uint32_t src = smem_u32(out) + buf * (2 * kReadHalfBytes);
+        tma_store_3d(map, src, 0, token, t.head());
+        tma_store_3d(map, src + kReadHalfBytes, 64, token, t.head());
+      }
+      bulk_commit();
+    }
+    buf ^= 1;
   }
+  if (lane == 0) bulk_wait_done();
 }
 
 // A page's codes (and scales) of all heads are contiguous: four block copies
@@ -408,17 +455,18 @@ cudaError_t launch_paged_append(const PagedArgs &p, const h3kv_rows &K, const h3
 
 cudaError_t launch_paged_read(const PagedArgs &p, const int32_t *rows, int64_t n, const h3kv_rows &K,
                               const h3kv_rows &V, const ServeDevice &d, cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  if (!encode_rows_bf16(&tk, K, p.kv_heads, n, kReadRows) || !encode_rows_bf16(&tv, V, p.kv_heads, n, kReadRows))
+    return cudaErrorInvalidValue;
+  // whole 32-byte sectors per load where the codes' alignment allows
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.k_codes) | reinterpret_cast<uintptr_t>(p.v_codes)) & 31) == 0;
+  auto kernel = wide ? read_kernel<true> : read_kernel<false>;
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t e = allow_smem(kernel, kReadSmemBytes, allowed[wide]);
+  if (e != cudaSuccess) return e;
   const int64_t tiles = (n + kTokens - 1) / kTokens * p.kv_heads * 2;
   const unsigned grid = static_cast<unsigned>(tiles < 2 * d.num_sms ? tiles : 2 * d.num_sms);
-  // whole 32-byte sectors per load and store where the alignment allows
-  auto low_bits = [&](const h3kv_rows &r) {
-    return reinterpret_cast<uintptr_t>(r.data) | static_cast<uintptr_t>(r.head_stride * 2) |
-           static_cast<uintptr_t>(r.row_stride * 2);
-  };
-  const bool wide = ((reinterpret_cast<uintptr_t>(p.k_codes) | reinterpret_cast<uintptr_t>(p.v_codes) | low_bits(K) |
-                      low_bits(V)) &
-                     31) == 0;
-  (wide ? read_kernel<true> : read_kernel<false>)<<<grid, kThreads, 0, stream>>>(p, rows, n, K, V);
+  kernel<<<grid, kThreads, kReadSmemBytes, stream>>>(tk, tv, p, rows, n);
   return cudaGetLastError();
 }
 
