@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
 // whole lines (written in 32-byte pieces from registers, 4.46 TB/s became 4.93).
 // 65536 rows of 8 heads: 75.6 us, 5.35 TB/s; 217088: 237 us, 5.65 TB/s.  Codes
 // brought to shared memory by asynchronous copies, three tiles ahead, were 3 %
-// slower: 48 shuffles and copies more a tile, with 16 warps an SM that issue in
+// slower: more instructions for a tile, with 16 warps an SM that issue in
 // 57 % of the cycles already.
 constexpr int kReadRows = 16;                       // rows of a warp in a tile
 constexpr int kReadHalfBytes = kReadRows * 128;     // 64 channels of them
