@@ -87,7 +87,7 @@ __device__ __forceinline__ Counts counts_of(const TreeArgs &a, int i) {
   c.len = on ? static_cast<int32_t>(len) : 0;
   c.nodes = on ? static_cast<int32_t>(m) : 0;
   c.tiles = (c.len + kBN - 1) / kBN;
-  c.row_tiles = (c.nodes * a.group + a.item_rows - 1) / a.item_rows;  // 0 without nodes
+  c.row_tiles = (c.nodes * a.group + a.item_rows - 1) >> (31 - __clz(a.item_rows));  // 0 without nodes
   c.units = static_cast<int64_t>(c.tiles + a.item_cost) * c.row_tiles * a.p.kv_heads;
   return c;
 }
@@ -232,30 +232,33 @@ struct Walk {
 using TreeSegs = SegRing<2>;
 using TreeReader = SegReader<TreeSegs>;
 
-// The walking warp.  Where its first segment goes on with an item that began on
-// the CTA before, it describes the item to the join.
+// Describes the item that the CTA's run goes on with, where it began on the CTA
+// before, to the join.
+__device__ __forceinline__ Split split_of(const TreeArgs &a, const Scan &sc) {
+  Split split = {};
+  const int size = sc.c.tiles + a.item_cost, cta = static_cast<int>(blockIdx.x);
+  const int64_t item = (sc.u0 - sc.before) / size;
+  // its tiles' units
+  const int64_t first = sc.before + item * size + a.item_cost, last = first + sc.c.tiles - 1;
+  if (sc.u0 > first && owner_of(sc.total, first, sc.ctas) == cta - 1) {
+    split.q_base = sc.c.q_base;
+    split.parts = owner_of(sc.total, last, sc.ctas) - cta + 2;
+    split.head = static_cast<int>(item / sc.c.row_tiles);
+    split.row0 = static_cast<int>(item - static_cast<int64_t>(split.head) * sc.c.row_tiles) * a.item_rows;
+    const int rows = sc.c.nodes * a.group - split.row0;
+    split.rows = rows < a.item_rows ? rows : a.item_rows;
+  }
+  return split;
+}
+
+// The walking warp.  (The others wait for the first segment: it goes out before
+// anything else is done.)
 __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &sc, const Workspace &ws,
                                                  TreeSegs &ring, const WaitCtx &w) {
   Walk walk;
   walk.start(a, sc);
-  Split split = {};
-  {
-    const int size = walk.c.tiles + a.item_cost;
-    const int64_t item = (walk.u - walk.before) / size;
-    // its tiles' units
-    const int64_t first = walk.before + item * size + a.item_cost, last = first + walk.c.tiles - 1;
-    const int cta = static_cast<int>(blockIdx.x);
-    if (walk.u > first && owner_of(sc.total, first, sc.ctas) == cta - 1) {
-      split.q_base = walk.c.q_base;
-      split.parts = owner_of(sc.total, last, sc.ctas) - cta + 2;
-      split.head = static_cast<int>(item / walk.c.row_tiles);
-      split.row0 = static_cast<int>(item - static_cast<int64_t>(split.head) * walk.c.row_tiles) * a.item_rows;
-      const int rows = walk.c.nodes * a.group - split.row0;
-      split.rows = rows < a.item_rows ? rows : a.item_rows;
-    }
-    if ((threadIdx.x & 31) == 0) ws.split[cta] = split;
-  }
   Ring<TreeSegs::kDepth> r;
+  bool described = false;
   for (;;) {
     Seg s;
     const bool more = walk.next(a, &s);
@@ -265,6 +268,11 @@ __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &
       mbar_arrive(smem_u32(&ring.full[r.slot]));
     }
     __syncwarp();
+    if (!described) {
+      described = true;
+      const Split split = split_of(a, sc);
+      if ((threadIdx.x & 31) == 0) ws.split[blockIdx.x] = split;
+    }
     if (!more) return;
     r.next();
   }
