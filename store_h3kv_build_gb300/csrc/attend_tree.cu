@@ -342,82 +342,89 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
 }
 
 // Joins the items that lie on several CTAs: block column b takes the one that
-// CTA b is the second of.  A warp takes 4 rows; where an item has fewer rows
-// than the block's 8 warps hold, the warps share its parts (warp w of `ways`
-// takes parts w, w + ways, ..) and meet in shared memory.  Parts are added in a
-// fixed order.
-constexpr int kJoinWarps = 8, kJoinRows = 4;
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const TreeArgs a) {
-  __shared__ float4 sh_o[kJoinWarps][kJoinRows][32];
-  __shared__ float2 sh_ml[kJoinWarps][kJoinRows];
+// CTA b + 1 is the second of.  A warp takes 4 rows, 8 lanes each, in the order
+// of fwht128_oct; where an item has fewer rows than the block's warps hold, the
+// warps share its parts (warp w of `ways` takes parts w, w + ways, ..) and meet
+// in shared memory.  Parts are added in a fixed order.
+constexpr int kJoinRows = 4, kJoinWarpsFew = 16, kJoinWarpsMany = 4;
+__global__ void __launch_bounds__(kJoinWarpsFew * 32) join_kernel(const TreeArgs a) {
+  extern __shared__ float4 sh_o[];  // [warps][4][32], if the warps share parts
+  __shared__ float2 sh_ml[kJoinWarpsFew][kJoinRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x + 1;
+  const int l8 = lane & 7, sub = lane >> 3, warps = blockDim.x >> 5;
   // (no thread leaves before this, so the grids end in stream order)
   pdl_wait_prerequisites();
   const Workspace ws = workspace_of(a);
   const Split sp = ws.split[b];
   if (sp.parts == 0) return;
-  const int groups = ws.rows <= 4 ? 1 : ws.rows <= 8 ? 2 : ws.rows <= 16 ? 4 : 8, ways = kJoinWarps / groups;
-  const int g = warp % groups, way = warp / groups;
-  const int r0 = (blockIdx.y * groups + g) * kJoinRows;
+  const int groups = ws.rows <= 4 ? 1 : ws.rows <= 8 ? 2 : 4, ways = warps / groups;
+  const int g = warp & (groups - 1), way = warp / groups;
+  const int r = (blockIdx.y * groups + g) * kJoinRows + sub;
+  const bool live = r < sp.rows;
   const float c2 = a.scale_log2;
-  float m[kJoinRows], l[kJoinRows];
-  float4 o[kJoinRows];
+  float m = kNoMax, l = 0.f, o[16];
 #pragma unroll
-  for (int i = 0; i < kJoinRows; ++i) {
-    m[i] = kNoMax;
-    l[i] = 0.f;
-    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  auto add = [&](int i, float2 ml, float4 p) {
-    const float mn = fmaxf(m[i], ml.x), ga = ex2((m[i] - mn) * c2), gb = ex2((ml.x - mn) * c2);
-    l[i] = fmaf(l[i], ga, ml.y * gb);
-    o[i].x = fmaf(o[i].x, ga, p.x * gb);
-    o[i].y = fmaf(o[i].y, ga, p.y * gb);
-    o[i].z = fmaf(o[i].z, ga, p.z * gb);
-    o[i].w = fmaf(o[i].w, ga, p.w * gb);
-    m[i] = mn;
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+  auto add = [&](float2 ml, const float (&p)[16]) {
+    const float mn = fmaxf(m, ml.x), ga = ex2((m - mn) * c2), gb = ex2((ml.x - mn) * c2);
+    l = fmaf(l, ga, ml.y * gb);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = fmaf(o[e], ga, p[e] * gb);
+    m = mn;
   };
+  if (live) {
 #pragma unroll 2
-  for (int k = way; k < sp.parts; k += ways) {
-    const int64_t at = (static_cast<int64_t>(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * ws.rows + r0;
-    float2 ml[kJoinRows];
-    float4 p[kJoinRows];
+    for (int k = way; k < sp.parts; k += ways) {
+      const int64_t at = (static_cast<int64_t>(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * ws.rows + r;
+      const float4 *src = reinterpret_cast<const float4 *>(ws.o + at * 128) + 2 * l8;
+      const float2 ml = ws.ml[at];
+      float p[16];
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) {
-      if (r0 + i < sp.rows) {
-        ml[i] = ws.ml[at + i];
-        p[i] = reinterpret_cast<const float4 *>(ws.o + (at + i) * 128)[lane];
+      for (int x = 0; x < 4; ++x) {
+        const float4 f = src[(x >> 1) * 16 + (x & 1)];
+        p[4 * x] = f.x;
+        p[4 * x + 1] = f.y;
+        p[4 * x + 2] = f.z;
+        p[4 * x + 3] = f.w;
       }
+      add(ml, p);
     }
-#pragma unroll
-    for (int i = 0; i < kJoinRows; ++i)
-      if (r0 + i < sp.rows) add(i, ml[i], p[i]);
   }
   if (ways > 1) {
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) {
-      sh_o[warp][i][lane] = o[i];
-      if (lane == 0) sh_ml[warp][i] = make_float2(m[i], l[i]);
-    }
+    for (int x = 0; x < 4; ++x)
+      sh_o[(warp * 4 + x) * 32 + lane] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+    if (l8 == 0) sh_ml[warp][sub] = make_float2(m, l);
     __syncthreads();
     if (way > 0) return;
-    for (int x = 1; x < ways; ++x) {
+    for (int y = 1; y < ways; ++y) {
+      const int from = y * groups + g;
+      float p[16];
 #pragma unroll
-      for (int i = 0; i < kJoinRows; ++i) add(i, sh_ml[x * groups + g][i], sh_o[x * groups + g][i][lane]);
+      for (int x = 0; x < 4; ++x) {
+        const float4 f = sh_o[(from * 4 + x) * 32 + lane];
+        p[4 * x] = f.x;
+        p[4 * x + 1] = f.y;
+        p[4 * x + 2] = f.z;
+        p[4 * x + 3] = f.w;
+      }
+      add(sh_ml[from][sub], p);
     }
   }
+  fwht128_oct(o, l8);
+  if (!live) return;
+  const float inv = kInvSqrt128 / l;
+  const int x = sp.row0 + r, node = node_of(a, x), h = sp.head * a.group + (x - node * a.group);
+  const int64_t row = sp.q_base + node;
+  uint4 *dst = reinterpret_cast<uint4 *>(a.o.data + h * a.o.head_stride + row * a.o.row_stride) + l8;
 #pragma unroll
-  for (int i = 0; i < kJoinRows; ++i) {
-    if (r0 + i >= sp.rows) break;
-    float v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
-    fwht128_warp(v, lane);
-    const float inv = kInvSqrt128 / l[i];
-    const int x = sp.row0 + r0 + i, node = node_of(a, x), h = sp.head * a.group + (x - node * a.group);
-    const int64_t row = sp.q_base + node;
-    *reinterpret_cast<uint2 *>(a.o.data + h * a.o.head_stride + row * a.o.row_stride + 4 * lane) =
-        make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
-    if (a.lse && lane == 0) a.lse[h * a.nodes + row] = kLn2 * (m[i] * c2 + log2f(l[i]));
+  for (int hi = 0; hi < 2; ++hi) {
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = pack_bf16x2(o[8 * hi + 2 * k] * inv, o[8 * hi + 2 * k + 1] * inv);
+    dst[8 * hi] = make_uint4(c[0], c[1], c[2], c[3]);
   }
+  if (a.lse && l8 == 0) a.lse[h * a.nodes + row] = kLn2 * (m * c2 + log2f(l));
 }
 
 }  // namespace
@@ -454,9 +461,12 @@ cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (a.ctas < 2) return cudaSuccess;
   const int rows = part_rows(a.group, a.nodes, a.item_rows);
+  const bool few = rows <= 16;  // (one block an item)
+  const int warps = few ? kJoinWarpsFew : kJoinWarpsMany;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas - 1, (rows + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3(a.ctas - 1, few ? 1 : (rows + kJoinWarpsMany * kJoinRows - 1) / (kJoinWarpsMany * kJoinRows));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = few ? warps * kJoinRows * 32 * sizeof(float4) : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
