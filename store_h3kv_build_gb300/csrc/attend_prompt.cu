@@ -196,10 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t see[4];
           if (__any_sync(0xffffffffu, n < kBN)) {
             prefix_mask(n, see);
-            softmax_tile<false, true>(tS, tO, t == t_first, see, c2, row);
-          } else {
-            softmax_tile<false, false>(tS, tO, t == t_first, see, c2, row);
+            mask_tile(tS, see);
           }
+          softmax_tile<false>(tS, tO, t == t_first, c2, row);
         }
         tc_fence_before();
         __syncwarp();

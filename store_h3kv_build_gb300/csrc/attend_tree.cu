@@ -1,6 +1,7 @@
 // attend_tree.cu -- attention of drafted tokens over the paged kvi8r cache: the
 // kernel for many rows of a sequence and kv head (the tcgen05 pipeline of
 // serve_attend.cuh), the join, and the choice of kernel.
+#include "store_fwht.cuh"
 #include "tree.cuh"
 
 namespace h3kv {
@@ -177,10 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
           uint32_t see[4];
           if (pos + kBN > base_key) {
             tree_mask(pos, base_key, path, see);
-            softmax_tile<true, true>(tS, tO, t == t_first, see, c2, row);
-          } else {
-            softmax_tile<true, false>(tS, tO, t == t_first, see, c2, row);
+            mask_tile(tS, see);
           }
+          softmax_tile<true>(tS, tO, t == t_first, c2, row);
         }
         tc_fence_before();
         __syncwarp();
@@ -194,27 +194,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       if (e == kWrite) {
         const bool live = r < s.rows;
         if (s.whole) {
-          float o[128];
-          const float inv = kInvSqrt128 / row.l;
-          load_o(tO, tO + 128, joined, ga * inv, gb * inv, o);
-          fwht128_packed(o);
-          if (live) {
-            const int x = s.row0 + r, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
-            uint16_t *dst = a.o.data + h * a.o.head_stride + (s.q_base + node) * a.o.row_stride;
+          // H128 = [[H64, H64], [H64, -H64]]: the output's halves are the
+          // transforms of the sum and of the difference of O's; a loop over
+          // them (code of half the size, see mask_tile)
+          const float inv = kInvSqrt128 / row.l, gx = ga * inv, gy = gb * inv;
+          const int x = s.row0 + r, node = node_of(a, live ? x : 0), h = s.head * a.group + (x - node * a.group);
+          uint16_t *dst = a.o.data + h * a.o.head_stride + (s.q_base + node) * a.o.row_stride;
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            float o[64];
+            const float sx = hf ? -gx : gx, sy = hf ? -gy : gy;
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              uint32_t c[8];
+            for (int c = 0; c < 2; ++c) {
+              float lo[32], hi[32];
+              tmem_ld32(tO + c * 32, *reinterpret_cast<uint32_t(*)[32]>(lo));
+              tmem_ld32(tO + 64 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(hi));
 #pragma unroll
-              for (int k = 0; k < 8; ++k) c[k] = pack_bf16x2(o[16 * g + 2 * k], o[16 * g + 2 * k + 1]);
-              if constexpr (kWide) {
-                st_global_v8(dst + 16 * g, c);
-              } else {
-                reinterpret_cast<uint4 *>(dst)[2 * g] = make_uint4(c[0], c[1], c[2], c[3]);
-                reinterpret_cast<uint4 *>(dst)[2 * g + 1] = make_uint4(c[4], c[5], c[6], c[7]);
+              for (int k = 0; k < 32; ++k) o[32 * c + k] = fmaf(hi[k], sx, lo[k] * gx);
+            }
+            if (joined) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float lo[16], hi[16];
+                tmem_ld16(tO + 128 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(lo));
+                tmem_ld16(tO + 192 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(hi));
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[16 * c + k] += fmaf(hi[k], sy, lo[k] * gy);
               }
             }
-            if (a.lse) a.lse[h * a.nodes + s.q_base + node] = kLn2 * (row.m * c2 + log2f(row.l));
+            fwht64_packed(o);
+            if (live) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                uint32_t c[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) c[k] = pack_bf16x2(o[16 * g + 2 * k], o[16 * g + 2 * k + 1]);
+                uint16_t *to = dst + 64 * hf + 16 * g;
+                if constexpr (kWide) {
+                  st_global_v8(to, c);
+                } else {
+                  reinterpret_cast<uint4 *>(to)[0] = make_uint4(c[0], c[1], c[2], c[3]);
+                  reinterpret_cast<uint4 *>(to)[1] = make_uint4(c[4], c[5], c[6], c[7]);
+                }
+              }
+            }
           }
+          if (live && a.lse) a.lse[h * a.nodes + s.q_base + node] = kLn2 * (row.m * c2 + log2f(row.l));
         } else {
           const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (s.t0 > 0 ? 0 : 1)) * ws.rows + r;
           float *dst = ws.o + at * 128;

@@ -175,8 +175,7 @@ struct MmaState {
   uint32_t go, tmem, dhi, lq0, lk0, lv0, idesc_qk, idesc_pv;
   Ring<kNK> k;        // the next key tile whose QK is to be issued first
   Ring<kNV> v;
-  uint32_t p_phase[2] = {0, 0};
-  uint32_t q_phase[2] = {0, 0};
+  uint32_t p_phase = 0, q_phase = 0;  // bit q: of stream q
   uint32_t fix_phase = 0;
 };
 
@@ -192,20 +191,18 @@ __device__ __forceinline__ void mma_setup(MmaState &m, Smem &sm, bool bf16) {
   m.lv0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sm.v[0]), kChunkBytes, 1024));
 }
 
-__device__ __forceinline__ void issue_qk(const MmaState &m, int q, int ks) {
-  const uint32_t lq = m.lq0 + q * (kTileBytes >> 4), lk = m.lk0 + ks * (kTileBytes >> 4);
+__device__ __forceinline__ void issue_qk(const MmaState &m, uint32_t tS, uint32_t lq, uint32_t lk) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
-    mma_ss(m.go, m.tmem + q * 128, lq + off, lk + off, m.dhi, m.idesc_qk, kk > 0);
+    mma_ss(m.go, tS, lq + off, lk + off, m.dhi, m.idesc_qk, kk > 0);
   }
 }
 
-__device__ __forceinline__ void issue_pv(const MmaState &m, int q, int vs, bool acc) {
-  const uint32_t lv = m.lv0 + vs * (kTileBytes >> 4);
+__device__ __forceinline__ void issue_pv(const MmaState &m, uint32_t tS, uint32_t lv, uint32_t acc) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    mma_ts(m.go, m.tmem + 256 + q * 128, m.tmem + q * 128 + kk * 8, lv + (kk * 2048 >> 4), m.dhi, m.idesc_pv,
+    mma_ts(m.go, tS + 256, tS + kk * 8, lv + (kk * 2048 >> 4), m.dhi, m.idesc_pv,
            (acc || kk > 0) ? 1u : 0u);
 }
 
@@ -220,12 +217,12 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
   uint64_t *v_rdy = kReady ? sm.v_ready : sm.v_load;
   // the stream's QK of tile t: waits for the tile (its first user does), and
   // releases it after its last user
-  auto qk = [&](int q, bool first_user, bool last_user, bool last_qk) {
+  auto qk = [&](int q, uint32_t tS, uint32_t lq, uint32_t lk, bool first_user, bool last_user, bool last_qk) {
     if (first_user) {
       if (!warp_wait(smem_u32(&k_rdy[m.k.slot]), m.k.phase, w)) return false;
       tc_fence_after();
     }
-    issue_qk(m, q, m.k.slot);
+    issue_qk(m, tS, lq, lk);
     mma_commit(m.go, smem_u32(&sm.s_full[q]));
     if (last_user) {
       mma_commit(m.go, smem_u32(&sm.k_free[m.k.slot]));
@@ -234,14 +231,16 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
     if (last_qk) mma_commit(m.go, smem_u32(&sm.q_free[q]));
     return true;
   };
+#pragma unroll 1
   for (int q = 0; q < 2; ++q) {
     if (!has_tiles(s, q)) continue;
-    if (!warp_wait(smem_u32(&sm.q_full[q]), m.q_phase[q], w)) return false;
-    m.q_phase[q] ^= 1u;
+    if (!warp_wait(smem_u32(&sm.q_full[q]), (m.q_phase >> q) & 1u, w)) return false;
+    m.q_phase ^= 1u << q;
     tc_fence_after();
     // two: both streams start on tile 0 (stream 1 alone where stream 0 has none)
     const bool first_user = !s.two || q == 0 || s.n0 == 0;
-    if (!qk(q, first_user, !s.two || q == 1, first_tile(s, q) + tile_step(s) >= end_tile(s, q))) return false;
+    if (!qk(q, m.tmem + q * 128, m.lq0 + q * (kTileBytes >> 4), m.lk0 + m.k.slot * (kTileBytes >> 4), first_user,
+            !s.two || q == 1, first_tile(s, q) + tile_step(s) >= end_tile(s, q))) return false;
   }
   const int step = tile_step(s);
   for (int t = 0; t < s.n; ++t) {
@@ -253,23 +252,27 @@ __device__ __forceinline__ bool mma_segment(MmaState &m, Smem &sm, const Seg &s,
       if (!warp_wait(smem_u32(&sm.v_fixed), m.fix_phase, w)) return false;
       m.fix_phase ^= 1u;
     }
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       const int q = s.two ? i : (t & 1);
       if (!s.two && i == 1) break;
-      if (t >= end_tile(s, q)) continue;
-      if (!warp_wait(smem_u32(&sm.p_full[q]), m.p_phase[q], w)) return false;
-      m.p_phase[q] ^= 1u;
+      const int end = end_tile(s, q), tn = t + step;
+      if (t >= end) continue;
+      // everything that the products need is at hand before the wait
+      uint32_t tS = m.tmem + q * 128, lv = m.lv0 + m.v.slot * (kTileBytes >> 4), lq = m.lq0 + q * (kTileBytes >> 4),
+               lk = m.lk0 + m.k.slot * (kTileBytes >> 4), acc = t != first_tile(s, q);
+      const bool last = !s.two || q == 1, more = tn < end, first_user = !s.two || q == 0 || tn >= s.n0;
+      asm volatile("" : "+r"(tS), "+r"(lv), "+r"(lq), "+r"(lk), "+r"(acc));
+      if (!warp_wait(smem_u32(&sm.p_full[q]), (m.p_phase >> q) & 1u, w)) return false;
       tc_fence_after();
-      issue_pv(m, q, m.v.slot, t != first_tile(s, q));
-      if (!s.two || q == 1) mma_commit(m.go, smem_u32(&sm.v_free[m.v.slot]));
-      const int tn = t + step;
-      if (tn >= end_tile(s, q)) {
+      issue_pv(m, tS, lv, acc);
+      m.p_phase ^= 1u << q;
+      if (last) mma_commit(m.go, smem_u32(&sm.v_free[m.v.slot]));
+      if (!more) {
         mma_commit(m.go, smem_u32(&sm.o_full[q]));
-      } else {
-        const bool first_user = !s.two || q == 0 || tn >= s.n0;
-        if (!qk(q, first_user, !s.two || q == 1, tn + step >= end_tile(s, q))) return false;
+        continue;
       }
+      if (!qk(q, tS, lq, lk, first_user, last, tn + step >= end)) return false;
     }
     m.v.next();
   }
@@ -281,34 +284,35 @@ struct Row {
   float m, l;  // running maximum (raw score units) and sum of this thread's row
 };
 
-// One 128-key tile: S from TMEM, mask, running maximum, P back to TMEM.
-// kMasked: only the columns set in `see` count.
-template <bool kF16, bool kMasked>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, const uint32_t (&see)[4], float c2,
-                                             Row &r) {
-  float s[128];
-  float mt;
-  if constexpr (!kMasked) {
-    float m4[4];
-    tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
-    mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-  } else {
-    tmem_ld128(tS, *reinterpret_cast<uint32_t(*)[128]>(s));
+// Masks a tile's scores in TMEM: only the columns set in `see` count, whatever
+// the others hold.  A pass of its own, and a loop, because few tiles need it
+// and the kernels' code has to stay in the instruction caches.  With the mask in
+// a second copy of softmax_tile and the MMA issue unrolled over the streams, CTAs
+// that were at different places of their segments pushed each other's code out:
+// warps waited for instructions 2.5 cycles per issue (0.65 where all CTAs ran in
+// step), and 64 nodes over 128 x 2048 cached tokens took 411 us, now 338; 40
+// prompts of 300 tokens 85 us, now 76.
+__device__ __forceinline__ void mask_tile(uint32_t tS, const uint32_t (&see)[4]) {
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t bits = g == 0 ? see[0] : g == 1 ? see[1] : g == 2 ? see[2] : see[3];
+    if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+    uint32_t x[32];
+    tmem_ld32(tS + 32 * g, x);
 #pragma unroll
-    for (int c = 0; c < 128; ++c) s[c] = (see[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
-    float m8[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) m8[u] = fmax3(s[u], s[u + 8], s[u + 16]);
-#pragma unroll
-    for (int c = 24; c < 120; c += 16) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) m8[u] = fmax3(m8[u], s[c + u], s[c + 8 + u]);
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], s[120 + u]);
-    mt = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-    mt = fmaxf(mt, kNoMax);
+    for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : 0xff800000u;  // -infinity
+    tmem_st32(tS + 32 * g, x);
   }
+  tmem_wait_st();
+}
+
+// One 128-key tile: S from TMEM, running maximum, P back to TMEM.
+template <bool kF16>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, float c2, Row &r) {
+  float s[128];
+  float m4[4];
+  tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
+  const float mt = fmaxf(fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])), kNoMax);
   if (first) {
     r.m = mt;
     r.l = 0.f;
@@ -360,22 +364,6 @@ __device__ __forceinline__ void prefix_mask(int32_t n, uint32_t (&see)[4]) {
   for (int g = 0; g < 4; ++g) {
     const int32_t k = n - 32 * g;
     see[g] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
-  }
-}
-
-// The rows' O from TMEM times `ga`, plus stream 1's times `gb` when joined.
-__device__ __forceinline__ void load_o(uint32_t tO0, uint32_t tO1, bool joined, float ga, float gb, float (&o)[128]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float x[32];
-    tmem_ld32(tO0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
-#pragma unroll
-    for (int k = 0; k < 32; ++k) o[32 * c + k] = x[k] * ga;
-    if (joined) {
-      tmem_ld32(tO1 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x));
-#pragma unroll
-      for (int k = 0; k < 32; ++k) o[32 * c + k] = fmaf(x[k], gb, o[32 * c + k]);
-    }
   }
 }
 
