@@ -576,22 +576,19 @@ def _on_device(dev: int, call, *args, **kw):
         return call(*args, **kw)
 
 
-def _new_rows(stream, like: torch.Tensor, heads: int, rows: int) -> tuple[torch.Tensor, h3kv_rows]:
-    """A bf16 [heads, rows, 128] result, allocated on the call's stream (see
-    _on), and its C struct."""
-    if stream is None:
-        out = like.new_empty((heads, rows, HEAD_DIM), dtype=torch.bfloat16)
-    else:
-        with torch.cuda.stream(stream):
-            out = like.new_empty((heads, rows, HEAD_DIM), dtype=torch.bfloat16)
-    return out, h3kv_rows(out.data_ptr(), rows * HEAD_DIM if heads > 1 else 0, HEAD_DIM if rows > 1 else 0)
-
-
 def _new(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """An uninitialised tensor on `like`'s device, allocated on the call's
+    stream (see _on).  (torch.empty: new_empty takes twice its time.)"""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _new_rows(stream, like: torch.Tensor, heads: int, rows: int) -> tuple[torch.Tensor, h3kv_rows]:
+    """A bf16 [heads, rows, 128] result and its C struct."""
+    out = _new(stream, like, (heads, rows, HEAD_DIM), torch.bfloat16)
+    return out, h3kv_rows(out.data_ptr(), rows * HEAD_DIM if heads > 1 else 0, HEAD_DIM if rows > 1 else 0)
 
 
 @functools.lru_cache(maxsize=256)
