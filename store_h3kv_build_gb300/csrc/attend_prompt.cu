@@ -9,6 +9,12 @@
 // (cluster launch control), so that the next segment's copies and first
 // products run under the present one's output, and the hardware's order still
 // balances the SMs.
+//
+// Bound by the tensor cores and, beside them, by the softmax chain of the two
+// streams; short prompts by the tiles of 128 that they do not fill and by the
+// few segments there are.  Measured (causal): 16384 rows of 32 heads over 8 1.33
+// ms, 1650 TFLOP/s; of 8 over 2 353 us, 1556; 8 x 2048 rows 222 us, 1239; 8 x 512
+// 32 us, 544; 40 x 300 of 24 over 8 75 us, 296; one of 500 10.6 us.
 #include "serve_attend.cuh"
 
 namespace h3kv {

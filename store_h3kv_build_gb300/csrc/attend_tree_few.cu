@@ -17,7 +17,10 @@
 // 8 such warps; producer warps copy whole pages: codes by TMA with the 128-byte
 // swizzle (so that the reads below spread over the banks), scales by bulk
 // copies, kStages tiles of 33 KB in flight.  A step's codes are taken into
-// registers at once, so that a stage is empty while its products run.
+// registers at once, so that a stage is empty while its products run.  Measured,
+// 32 query heads over 8, one token each: 32 x 8192 cached rows 95.5 us (5.7 TB/s),
+// 8 x 32768 92 us (5.9), 256 x 1024 122 us (4.5), 1 x 65536 32 us (4.3), 1 x 1024 9
+// us; 5 tokens with 32 heads over 32 on 217088 rows 276 us (6.5 TB/s).
 #include "tree.cuh"
 
 namespace h3kv {

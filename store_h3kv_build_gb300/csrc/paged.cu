@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // A page's codes (and scales) of all heads are contiguous: four block copies
-// per page, cut into chunks of 16 KB, one CTA each.
+// per page, cut into chunks of 16 KB, one CTA each.  Bound by HBM: 1500 pages of
+// 64 rows and 8 heads 63.5 us, 6.29 TB/s; 24 pages 5.8 us, a call's latency.
 constexpr int kCopyChunk = 16384;
 
 __global__ void __launch_bounds__(kThreads)
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kThreads)
 // One CTA for a sequence and head.  A row may move onto one that is itself
 // kept and moves on, so every kept row is read into registers before any is
 // written: 64 rows x 2 tensors x 8 granules of 16 bytes = 1024, four per
-// thread.
+// thread.  Bound by latency: four dependent loads and a store.
 __global__ void __launch_bounds__(kThreads)
     keep_kernel(const PagedArgs p, const int32_t *__restrict__ table, const int64_t max_pages,
                 const int32_t *__restrict__ lengths, const int32_t *__restrict__ cu, const uint8_t *__restrict__ keep,

@@ -65,10 +65,14 @@ __device__ inline Workspace workspace_of(const TreeArgs &a) {
   return ws;
 }
 
-// What an item costs beside its key tiles (query rows, join, output), in tiles:
-// its first units, to which no tile belongs.  Measured: 1.5 us at 0.8 us a tile
-// for few rows, 8 us at 1.9 us for many.
-inline int item_cost_of(int32_t item_rows) { return item_rows == kManyRows ? 4 : 2; }
+// What an item costs beside its key tiles (query rows, first page, output, join),
+// in tiles: its first units, to which no tile belongs.  Sequences of very
+// different lengths tell: 33 of 64 .. 32768 cached rows, 32 heads over 8, took 91,
+// 80, 80 and 83 us at 2, 3, 4 and 6 tiles (one token each: items of 8 rows), 139,
+// 118, 104 and 106 (4 nodes: items of 16), and 243, 218 and 220 us at 4, 6 and 8
+// (64 nodes).  100 of 64 .. 8192: 102, 86, 88 and 93; 161, 129, 116 and 121; 278,
+// 268 and 280.
+inline int item_cost_of(int32_t item_rows) { return item_rows == kManyRows ? 6 : item_rows == 16 ? 4 : 3; }
 
 // A sequence's counts; tiles == 0: nothing to do (empty, or out of range).
 struct Counts {
