@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mma_commit(m.go, smem_u32(&sm.drain));
       mbar_wait_drain(smem_u32(&sm.drain), 0, kDrainNs);
     } else if (warp == 15) {
-      publish_segments(a, sm.scan, ws, sm.segs, w);
+      publish_segments(a, sm.scan, ws, sm.segs, w, [](const Seg &, int) { return true; });
     }
   }
   __syncwarp();

@@ -18,8 +18,8 @@
 // swizzle (so that the reads below spread over the banks), scales by bulk
 // copies, kStages tiles of 33 KB in flight.  A step's codes are taken into
 // registers at once, so that a stage is empty while its products run.  Measured,
-// 32 query heads over 8, one token each: 32 x 8192 cached rows 95.5 us (5.7 TB/s),
-// 8 x 32768 92 us (5.9), 256 x 1024 122 us (4.5), 1 x 65536 32 us (4.3), 1 x 1024 9
+// 32 query heads over 8, one token each: 32 x 8192 cached rows 94 us (5.8 TB/s),
+// 8 x 32768 92 us (5.9), 256 x 1024 111 us (4.9), 1 x 65536 32 us (4.3), 1 x 1024 9
 // us; 5 tokens with 32 heads over 32 on 217088 rows 276 us (6.5 TB/s).
 #include "tree.cuh"
 
@@ -39,10 +39,10 @@ struct FewSmem {
   uint8_t v[kStages][kCodeBytes];
   float o[kWarps][8][kPitch];              // the warps' O, 8 rows at a time
   uint16_t ks[kStages][kBN], vs[kStages][kBN];
-  uint16_t q[8 * kNT][128];                // q' of the segment's rows
+  uint16_t q[TreeSegs::kDepth][8 * kNT][128];  // q' of a segment's rows, by its slot
   float m[kWarps][8 * kNT], l[kWarps][8 * kNT];
-  uint64_t path[8 * kNT];
-  uint64_t full[kStages], empty[kStages];
+  uint64_t path[TreeSegs::kDepth][8 * kNT];
+  uint64_t full[kStages], empty[kStages], q_full[TreeSegs::kDepth];
   Scan scan;
   TreeSegs segs;
   int abort;
@@ -72,6 +72,20 @@ __device__ __forceinline__ uint32_t scale2(uint32_t x, uint32_t s) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// q' = fp16(q H) of a row in place, by 8 lanes (l: the lane among them).
+__device__ __forceinline__ void rotate_row(uint16_t (&row)[128], int l) {
+  uint4 *dst = reinterpret_cast<uint4 *>(row) + l;
+  float v[16];
+  unpack_bf16x8(dst[0], v);
+  unpack_bf16x8(dst[8], v + 8);
+  fwht128_oct(v, l);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] *= kInvSqrt128;
+  dst[0] = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+  dst[8] = make_uint4(pack_f16x2(v[8], v[9]), pack_f16x2(v[10], v[11]), pack_f16x2(v[12], v[13]),
+                      pack_f16x2(v[14], v[15]));
+}
+
 template <int kNT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
@@ -89,6 +103,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(smem_u32(&sm.empty[s]), 8);
     }
     init_seg_ring(sm.segs, kWarps + kProducers);
+    for (int i = 0; i < TreeSegs::kDepth; ++i) mbar_init(smem_u32(&sm.q_full[i]), 1);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -101,8 +116,34 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   TreeReader sr;
 
+  // The walking warp also fetches the query rows (rows behind them 0) and their
+  // paths while the consumers are still at the segment before: 256 sequences of
+  // 1024 rows 121 -> 115 us.  Of items of 8 rows it rotates them too, 111 us; of
+  // 16 rows it takes too long before the first segment (27.3 us for 4 nodes of 8
+  // sequences, against 26.4), so there each consumer rotates four.
+  constexpr bool kAhead = kNT == 1;
   if (warp == kWarps + kProducers) {
-    publish_segments(a, sm.scan, ws, sm.segs, w);
+    publish_segments(a, sm.scan, ws, sm.segs, w, [&](const Seg &s, int slot) {
+      const int l = lane & 7;
+#pragma unroll 1
+      for (int row = lane >> 3; row < 8 * kNT; row += 4) {
+        const bool in = row < s.rows;
+        const int x = s.row0 + (in ? row : 0), node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
+        const uint16_t *src = a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride + 8 * l;
+        const uint32_t dst = smem_u32(sm.q[slot][row]) + 16 * l;
+        copy16_async(dst, src, in);
+        copy16_async(dst + 128, src + 64, in);
+        if (l == 0) sm.path[slot][row] = in ? path_of(a, s.q_base, node) : 0;
+      }
+      copy16_wait();
+      if constexpr (kAhead) {
+#pragma unroll 1
+        for (int row = lane >> 3; row < 8 * kNT; row += 4) rotate_row(sm.q[slot][row], l);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
+      return true;
+    });
     return;
   }
   if (warp >= kWarps) {
@@ -174,32 +215,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   for (;;) {
     bool ok = sr.get(sm.segs, w);
     const Seg &s = sr.seg(sm.segs);
-    // q' = fp16(q H) of the segment's rows, rows behind them 0
-    if (ok && s.n > 0 && warp < 2 * kNT) {
-      const int row = warp * 4 + (lane >> 3), l = lane & 7;
-      uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (row < s.rows) {
-        const int x = s.row0 + row, node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
-        const uint4 *src =
-            reinterpret_cast<const uint4 *>(a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride) + l;
-        raw[0] = __ldg(src);
-        raw[1] = __ldg(src + 8);
-        if (l == 0) sm.path[row] = path_of(a, s.q_base, node);
-      } else if (l == 0) {
-        sm.path[row] = 0;
-      }
-      float v[16];
-      unpack_bf16x8(raw[0], v);
-      unpack_bf16x8(raw[1], v + 8);
-      fwht128_oct(v, l);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= kInvSqrt128;
-      uint4 *dst = reinterpret_cast<uint4 *>(sm.q[row]) + l;
-      dst[0] = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
-                          pack_f16x2(v[6], v[7]));
-      dst[8] = make_uint4(pack_f16x2(v[8], v[9]), pack_f16x2(v[10], v[11]), pack_f16x2(v[12], v[13]),
-                          pack_f16x2(v[14], v[15]));
-    }
+    const int qs = sr.r.slot;
+    if (ok && s.n > 0) ok = warp_wait(smem_u32(&sm.q_full[qs]), sr.r.phase, w);
+    if (!kAhead && ok && s.n > 0 && warp < 2 * kNT) rotate_row(sm.q[qs][warp * 4 + (lane >> 3)], lane & 7);
     // the warps go on, or leave, together
     ok = named_bar_and(1, kWarps * 32, ok);
     if (!ok || s.n == 0) break;
@@ -210,7 +228,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(&sm.q[8 * nt + g8][16 * (i4 + 4 * hf)]);
+        const uint4 *src = reinterpret_cast<const uint4 *>(&sm.q[qs][8 * nt + g8][16 * (i4 + 4 * hf)]);
         const uint4 x = src[0], y = src[1];
         uint32_t *d = qf[nt] + 8 * hf;
         d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w, d[4] = y.x, d[5] = y.y, d[6] = y.z, d[7] = y.w;
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint64_t path = sm.path[8 * nt + 2 * i4 + e];
+              const uint64_t path = sm.path[qs][8 * nt + 2 * i4 + e];
               if (n0 >= 0 && !(n0 < 64 && (path >> n0) & 1)) st[nt][e] = -INFINITY;
               if (n1 >= 0 && !(n1 < 64 && (path >> n1) & 1)) st[nt][2 + e] = -INFINITY;
             }

@@ -256,9 +256,11 @@ __device__ __forceinline__ Split split_of(const TreeArgs &a, const Scan &sc) {
 }
 
 // The walking warp.  (The others wait for the first segment: it goes out before
-// anything else is done.)
+// anything else is done.)  `then` is called behind each segment that went out,
+// with its slot, and says whether to go on.
+template <class Then>
 __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &sc, const Workspace &ws,
-                                                 TreeSegs &ring, const WaitCtx &w) {
+                                                 TreeSegs &ring, const WaitCtx &w, const Then &then) {
   Walk walk;
   walk.start(a, sc);
   Ring<TreeSegs::kDepth> r;
@@ -272,12 +274,13 @@ __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &
       mbar_arrive(smem_u32(&ring.full[r.slot]));
     }
     __syncwarp();
+    const bool go = more && then(s, r.slot);
     if (!described) {
       described = true;
       const Split split = split_of(a, sc);
       if ((threadIdx.x & 31) == 0) ws.split[blockIdx.x] = split;
     }
-    if (!more) return;
+    if (!go) return;
     r.next();
   }
 }
