@@ -368,6 +368,23 @@ def test_append_and_read_rows_out_of_range(cuda):
         same_store(st, ref)
 
 
+@pytest.mark.parametrize("n", [1, 15, 17, 128, 131, 400])
+def test_read_writes_its_rows_only(cuda, n):
+    st, _ = random_store(9, 3, 64)
+    rows = torch.randperm(9 * 64, generator=torch.Generator().manual_seed(n))[:n].to(torch.int32)
+    rows[n // 2] = -1
+    want = b.paged_read(st, rows.to(DEV))
+    by_head = torch.full((5, n + 9, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    by_token = torch.full((n + 9, 5, 256), 7.0, dtype=torch.bfloat16, device=DEV)
+    k, v = by_head[1:4, 5:5 + n], by_token[5:5 + n, 1:4, 64:192].transpose(0, 1)
+    got = b.paged_read(st, rows.to(DEV), k, v)
+    b.sync_status()
+    assert got[0] is k and got[1] is v and torch.equal(k, want[0]) and torch.equal(v, want[1])
+    k.fill_(7.0)
+    v.fill_(7.0)
+    assert (by_head == 7).all() and (by_token == 7).all()
+
+
 @pytest.mark.parametrize("heads,ps,n", [(1, 16, 1), (8, 64, 3), (3, 32, 7), (32, 128, 2)])
 def test_copy_pages(cuda, heads, ps, n):
     st, ref = random_store(2 * n + 2, heads, ps, seed=n)
@@ -505,6 +522,21 @@ def test_tree_many_sequences_of_many_rows(cuda):
     lens = g.integers(10, 120, 620).tolist()
     nodes = [int(g.integers(5, min(n, 14) + 1)) for n in lens]
     tree_case(lens, nodes, 4, 1, 16, seed=6)
+
+
+@pytest.mark.parametrize("hq,hk", [(4, 1), (32, 1), (19, 1), (8, 2)])
+def test_tree_between_few_and_many_rows(cuda, hq, hk):
+    # a mean of 17 to 32 rows a sequence and kv head: items of 16 rows, some
+    # sequences with many of them
+    g = np.random.default_rng(hq)
+    n = 40 if hq < 16 else 12
+    lens = g.integers(64, 700, n).tolist()
+    nodes = [int(g.integers(1, 9)) for _ in lens] if hq < 16 else [1] * n
+    nodes[3], nodes[7] = (64, 0) if hq < 16 else (1, 0)
+    mean = sum(nodes) * (hq // hk) / n
+    assert 16 < mean <= 32
+    tree_case(lens, nodes, hq, hk, 32, seed=hq)
+    tree_case([30000], [32 // (hq // hk)], hq, hk, 64, seed=9)
 
 
 def test_tree_long_cache(cuda):
