@@ -56,25 +56,40 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 w, float *x) {
 // 64 hi + 8 l + e of the row is x[8 hi + e] of the group's lane l, so that a
 // row's loads and stores are two runs of 8 lanes x 16 bytes.  Strides 1, 2, 4
 // and 64 run in registers, strides 8, 16, 32 between lanes: 48 shuffles for
-// the warp's 4 rows, against 80 with a row across the warp.
+// the warp's 4 rows, against 80 with a row across the warp.  All but stride 1
+// take two values an instruction (a - b as fma(b, -1, a), the same rounding).
 __device__ __forceinline__ void fwht128_oct(float (&x)[16], int l) {
+  const float2 neg = make_float2(-1.f, -1.f);
 #pragma unroll
-  for (int h = 1; h < 16; h <<= 1) {
+  for (int i = 0; i < 16; i += 2) {
+    const float a = x[i], b = x[i + 1];
+    x[i] = a + b;
+    x[i + 1] = a - b;
+  }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+  for (int h = 2; h < 16; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
       if ((i & h) == 0) {
-        const float a = x[i], b = x[i + h];
-        x[i] = a + b;
-        x[i + h] = a - b;
+        const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[i + h], x[i + h + 1]);
+        const float2 s = __fadd2_rn(a, b), d = __ffma2_rn(b, neg, a);
+        x[i] = s.x;
+        x[i + 1] = s.y;
+        x[i + h] = d.x;
+        x[i + h + 1] = d.y;
       }
     }
   }
 #pragma unroll
   for (int m = 1; m < 8; m <<= 1) {
+    const float sg = (l & m) ? -1.f : 1.f;
+    const float2 sign = make_float2(sg, sg);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
-      x[i] = (l & m) ? o - x[i] : x[i] + o;
+    for (int i = 0; i < 16; i += 2) {
+      const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, x[i], m), __shfl_xor_sync(0xffffffffu, x[i + 1], m));
+      const float2 z = __ffma2_rn(make_float2(x[i], x[i + 1]), sign, o);
+      x[i] = z.x;
+      x[i + 1] = z.y;
     }
   }
 }
