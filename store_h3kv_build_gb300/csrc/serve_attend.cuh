@@ -290,8 +290,8 @@ struct Row {
 // a second copy of softmax_tile and the MMA issue unrolled over the streams, CTAs
 // that were at different places of their segments pushed each other's code out:
 // warps waited for instructions 2.5 cycles per issue (0.65 where all CTAs ran in
-// step), and 64 nodes over 128 x 2048 cached tokens took 411 us, now 338; 40
-// prompts of 300 tokens 85 us, now 76.
+// step), and 64 nodes over 128 x 2048 cached tokens took 411 us, then 338; 40
+// prompts of 300 tokens 85 us, then 76.
 __device__ __forceinline__ void mask_tile(uint32_t tS, const uint32_t (&see)[4]) {
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {

@@ -25,10 +25,11 @@ constexpr int kManyRows = 256;
 
 // Which of them, by the mean rows of a sequence and kv head (the host does not
 // know the single counts; every kernel is right for all of them).  Measured at
-// 32 x 8192 and 1 x 32768 cached tokens, 8 kv heads, 4 query heads each: 8 rows
-// 97 us in items of 8; 16 rows 124 and 28 us in items of 16, 180 and 30 in two of
-// 8; 32 rows 232 and 39 us in two items of 16, 242 and 48 on the pipeline; 40
-// rows 338 and 51 in three items of 16, 246 and 48 on the pipeline.
+// 32 x 8192, 1 x 32768 and 128 x 1024 cached tokens, 8 kv heads, 4 query heads
+// each: 8 rows 95, 20 and 62 us in items of 8, 123, 24 and 83 in items of 16; 16
+// rows 124, 26 and 87 us in items of 16, 176, 30 and 111 in two of 8; 32 rows
+// 234, 38 and 162 us in two items of 16, 236, 43 and 215 on the pipeline; 40 rows
+// 342, 50 and 235 us in three items of 16, 239, 43 and 221 on the pipeline.
 inline int item_rows_of(int32_t group, int64_t nodes, int32_t seqs) {
   const int64_t mean = (group * nodes + seqs - 1) / (seqs > 0 ? seqs : 1);
   return mean <= 8 ? 8 : mean <= 32 ? 16 : kManyRows;
