@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(kJoinWarpsFew * 32) join_kernel(const TreeArgs
   const Workspace ws = workspace_of(a);
   const Split sp = ws.split[b];
   if (sp.parts == 0) return;
-  const int groups = ws.rows <= 4 ? 1 : ws.rows <= 8 ? 2 : 4, ways = warps / groups;
-  const int g = warp & (groups - 1), way = warp / groups;
+  const int lg = ws.rows <= 4 ? 0 : ws.rows <= 8 ? 1 : ws.rows <= 16 || warps == 4 ? 2 : 3, groups = 1 << lg, ways = warps >> lg;
+  const int g = warp & (groups - 1), way = warp >> lg;
   const int r = (blockIdx.y * groups + g) * kJoinRows + sub;
   const bool live = r < sp.rows;
   const float c2 = a.scale_log2;
@@ -494,7 +494,7 @@ cudaError_t launch_attend_tree(const TreeArgs &args, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (a.ctas < 2) return cudaSuccess;
   const int rows = part_rows(a.group, a.nodes, a.item_rows);
-  const bool few = rows <= 16;  // (one block an item)
+  const bool few = rows <= 32;  // (one block an item)
   const int warps = few ? kJoinWarpsFew : kJoinWarpsMany;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas - 1, few ? 1 : (rows + kJoinWarpsMany * kJoinRows - 1) / (kJoinWarpsMany * kJoinRows));

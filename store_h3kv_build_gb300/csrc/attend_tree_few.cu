@@ -1,9 +1,9 @@
 // attend_tree_few.cu -- attention of drafted tokens over the paged kvi8r cache
-// for few rows of a sequence and kv head (at most 8 or 16: single tokens with
-// grouped heads, short drafts).
+// for few rows of a sequence and kv head (items of 8, 16 or 32: single tokens
+// with grouped heads, short drafts).
 //
 // Bound by HBM: 260 bytes of cache per key and kv head, against 4 * 128 FLOP
-// for each of at most 16 rows.  The 128-row tiles of tcgen05 would be nearly
+// for each of at most 32 rows.  The 128-row tiles of tcgen05 would be nearly
 // empty and would want K and V as fp16 in shared memory, twice the bytes of
 // the codes; here the codes go from shared memory to registers, are
 // dequantised there and feed warp-level MMAs (m16n8k16) whose 16 is the key
@@ -20,7 +20,9 @@
 // registers at once, so that a stage is empty while its products run.  Measured,
 // 32 query heads over 8, one token each: 32 x 8192 cached rows 94 us (5.8 TB/s),
 // 8 x 32768 92 us (5.9), 256 x 1024 111 us (4.9), 1 x 65536 32 us (4.3), 1 x 1024 9
-// us; 5 tokens with 32 heads over 32 on 217088 rows 276 us (6.5 TB/s).
+// us; 5 tokens with 32 heads over 32 on 217088 rows 273 us (6.6 TB/s).  Four tokens
+// each of 32 x 8192 124 us, eight 161 us: from 16 rows on the issue of the
+// products and of what feeds them bounds it.
 #include "tree.cuh"
 
 namespace h3kv {
@@ -32,6 +34,7 @@ constexpr int kWarps = 8, kProducers = 3, kStages = 5;
 constexpr int kFewThreads = (kWarps + kProducers + 1) * 32;
 constexpr int kCodeBytes = kBN * 128;      // one tile's codes
 constexpr int kPitch = 132;                // floats of a row in the join buffer
+constexpr int kQPitch = 136;               // values of a query row: 16 bytes aside, so that 8 rows' reads spread
 
 template <int kNT>
 struct FewSmem {
@@ -39,7 +42,7 @@ struct FewSmem {
   uint8_t v[kStages][kCodeBytes];
   float o[kWarps][8][kPitch];              // the warps' O, 8 rows at a time
   uint16_t ks[kStages][kBN], vs[kStages][kBN];
-  uint16_t q[TreeSegs::kDepth][8 * kNT][128];  // q' of a segment's rows, by its slot
+  uint16_t q[TreeSegs::kDepth][8 * kNT][kQPitch];  // q' of a segment's rows, by its slot
   float m[kWarps][8 * kNT], l[kWarps][8 * kNT];
   uint64_t path[TreeSegs::kDepth][8 * kNT];
   uint64_t full[kStages], empty[kStages], q_full[TreeSegs::kDepth];
@@ -73,7 +76,7 @@ __device__ __forceinline__ uint32_t scale2(uint32_t x, uint32_t s) {
 }
 
 // q' = fp16(q H) of a row in place, by 8 lanes (l: the lane among them).
-__device__ __forceinline__ void rotate_row(uint16_t (&row)[128], int l) {
+__device__ __forceinline__ void rotate_row(uint16_t (&row)[kQPitch], int l) {
   uint4 *dst = reinterpret_cast<uint4 *>(row) + l;
   float v[16];
   unpack_bf16x8(dst[0], v);
@@ -85,6 +88,13 @@ __device__ __forceinline__ void rotate_row(uint16_t (&row)[128], int l) {
   dst[8] = make_uint4(pack_f16x2(v[8], v[9]), pack_f16x2(v[10], v[11]), pack_f16x2(v[12], v[13]),
                       pack_f16x2(v[14], v[15]));
 }
+
+// Items of 32 rows: O of a thread takes 128 registers, so the consumers get 224,
+// the query fragments are read again for each tile and V's codes only behind
+// K's products.  (In two items of 16 rows, 8 nodes of four heads over 32 x 8192
+// rows took 234 us; 161 so.)
+constexpr uint32_t kRegConsumer = 224, kRegOther = 56;
+static_assert(2 * kRegConsumer + kRegOther == 3 * 168, "register split");
 
 template <int kNT>
 __global__ void __launch_bounds__(kFewThreads, 1)
@@ -121,32 +131,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   // 1024 rows 121 -> 115 us.  Of items of 8 rows it rotates them too, 111 us; of
   // 16 rows it takes too long before the first segment (27.3 us for 4 nodes of 8
   // sequences, against 26.4), so there each consumer rotates four.
-  constexpr bool kAhead = kNT == 1;
-  if (warp == kWarps + kProducers) {
-    publish_segments(a, sm.scan, ws, sm.segs, w, [&](const Seg &s, int slot) {
-      const int l = lane & 7;
-#pragma unroll 1
-      for (int row = lane >> 3; row < 8 * kNT; row += 4) {
-        const bool in = row < s.rows;
-        const int x = s.row0 + (in ? row : 0), node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
-        const uint16_t *src = a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride + 8 * l;
-        const uint32_t dst = smem_u32(sm.q[slot][row]) + 16 * l;
-        copy16_async(dst, src, in);
-        copy16_async(dst + 128, src + 64, in);
-        if (l == 0) sm.path[slot][row] = in ? path_of(a, s.q_base, node) : 0;
-      }
-      copy16_wait();
-      if constexpr (kAhead) {
-#pragma unroll 1
-        for (int row = lane >> 3; row < 8 * kNT; row += 4) rotate_row(sm.q[slot][row], l);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
-      return true;
-    });
-    return;
-  }
+  constexpr bool kAhead = kNT == 1, kBig = kNT == 4;
   if (warp >= kWarps) {
+    if constexpr (kBig) reg_dealloc<kRegOther>();
+    if (warp == kWarps + kProducers) {
+      publish_segments(a, sm.scan, ws, sm.segs, w, [&](const Seg &s, int slot) {
+        const int l = lane & 7;
+#pragma unroll 1
+        for (int row = lane >> 3; row < 8 * kNT; row += 4) {
+          const bool in = row < s.rows;
+          const int x = s.row0 + (in ? row : 0), node = node_of(a, x), h = s.head * a.group + (x - node * a.group);
+          const uint16_t *src = a.q.data + h * a.q.head_stride + (s.q_base + node) * a.q.row_stride + 8 * l;
+          const uint32_t dst = smem_u32(sm.q[slot][row]) + 16 * l;
+          copy16_async(dst, src, in);
+          copy16_async(dst + 128, src + 64, in);
+          if (l == 0) sm.path[slot][row] = in ? path_of(a, s.q_base, node) : 0;
+        }
+        copy16_wait();
+        if constexpr (kAhead) {
+#pragma unroll 1
+          for (int row = lane >> 3; row < 8 * kNT; row += 4) rotate_row(sm.q[slot][row], l);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
+        return true;
+      });
+      return;
+    }
     // =========================================================== producers
     // one warp each for K's codes, V's codes and the scales (one warp for all
     // of them was what bounded the kernel); lanes 0-7 take the pages of a
@@ -205,6 +216,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 
   // ============================================================= consumers
+  if constexpr (kBig) reg_alloc<kRegConsumer>();
   const int g8 = lane >> 2, i4 = lane & 3;   // MMA: row group and column pair
   const int key0 = warp * 16;          // its keys in a tile
   const float c2 = a.scale_log2;
@@ -223,15 +235,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (!ok || s.n == 0) break;
     // B fragments of q'^T: of row g8 the 16 channels of chunk i4 (and i4 + 4),
     // four of them for each k step: the channel order that K's chunks give
-    uint32_t qf[kNT][16];
+    uint32_t qf[kBig ? 1 : kNT][16];
+    auto fragments = [&](int nt, int hf, uint32_t *d) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(&sm.q[qs][8 * nt + g8][16 * (i4 + 4 * hf)]);
+      const uint4 x = src[0], y = src[1];
+      d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w, d[4] = y.x, d[5] = y.y, d[6] = y.z, d[7] = y.w;
+    };
+    if constexpr (!kBig) {
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(&sm.q[qs][8 * nt + g8][16 * (i4 + 4 * hf)]);
-        const uint4 x = src[0], y = src[1];
-        uint32_t *d = qf[nt] + 8 * hf;
-        d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w, d[4] = y.x, d[5] = y.y, d[6] = y.z, d[7] = y.w;
+      for (int nt = 0; nt < kNT; ++nt) {
+        fragments(nt, 0, qf[nt]);
+        fragments(nt, 1, qf[nt] + 8);
       }
     }
     const int32_t base_key = static_cast<int32_t>(s.keys) - s.nodes;
@@ -255,28 +269,32 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // the step's codes and scales into registers, and the stage is free again
       uint4 kw[2][2], vw[4];
       uint32_t k0, k1, v0, v1;
+      auto load_v = [&] {
+        const uint8_t *vb = sm.v[r.slot] + v_row;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t row = 2 * i4 + (x & 1);  // mod 8 (keys 8 later: the same)
+          vw[x] = *reinterpret_cast<const uint4 *>(vb + ((x & 1) + 8 * (x >> 1)) * 128 + ((g8 ^ row) << 4));
+        }
+        v0 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4]);
+        v1 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4 + 8]);
+        __syncwarp();
+        // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
+        if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.empty[r.slot]));
+        r.next();
+      };
       {
-        const uint8_t *kb = sm.k[r.slot] + k_row, *vb = sm.v[r.slot] + v_row;
+        const uint8_t *kb = sm.k[r.slot] + k_row;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint32_t c = ((i4 + 4 * hf) ^ k_x) << 4;
           kw[hf][0] = *reinterpret_cast<const uint4 *>(kb + c);
           kw[hf][1] = *reinterpret_cast<const uint4 *>(kb + 8 * 128 + c);
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t row = 2 * i4 + (x & 1);  // mod 8 (keys 8 later: the same)
-          vw[x] = *reinterpret_cast<const uint4 *>(vb + ((x & 1) + 8 * (x >> 1)) * 128 + ((g8 ^ row) << 4));
-        }
         k0 = sm.ks[r.slot][key0 + g8] * 0x10001u;
         k1 = sm.ks[r.slot][key0 + g8 + 8] * 0x10001u;
-        v0 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4]);
-        v1 = *reinterpret_cast<const uint32_t *>(&sm.vs[r.slot][key0 + 2 * i4 + 8]);
       }
-      __syncwarp();
-      // (a diagnostic may withhold one tile's arrival: see withhold_p_tile1)
-      if (lane == 0 && t + 1 != a.withhold_p_tile1) mbar_arrive(smem_u32(&sm.empty[r.slot]));
-      r.next();
+      if (!kBig || pos >= keys) load_v();
       if (pos < keys) {
         // S^T: keys g8 and g8 + 8, rows 2 i4 + {0, 1}; the channels in two
         // sums, so that the MMAs wait less for one another
@@ -286,8 +304,32 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           st[nt][0] = st[nt][1] = st[nt][2] = st[nt][3] = 0.f;
           su[nt][0] = su[nt][1] = su[nt][2] = su[nt][3] = 0.f;
         }
+        if constexpr (kBig) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint4 x = kw[hf][0], y = kw[hf][1];
+            uint32_t af[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t ux = (j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w) ^ 0x80808080u;
+              const uint32_t uy = (j == 0 ? y.x : j == 1 ? y.y : j == 2 ? y.z : y.w) ^ 0x80808080u;
+              af[j][0] = scale2(unbias(__byte_perm(ux, 0x64646464u, 0x4140)), k0);
+              af[j][1] = scale2(unbias(__byte_perm(uy, 0x64646464u, 0x4140)), k1);
+              af[j][2] = scale2(unbias(__byte_perm(ux, 0x64646464u, 0x4342)), k0);
+              af[j][3] = scale2(unbias(__byte_perm(uy, 0x64646464u, 0x4342)), k1);
+            }
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              uint32_t d[8];
+              fragments(nt, hf, d);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma16816(st[nt], af[j], d[2 * j], d[2 * j + 1]);
+            }
+          }
+          load_v();
+        }
+#pragma unroll
+        for (int j = 0; j < (kBig ? 0 : 4); ++j) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint4 x = kw[hf][0], y = kw[hf][1];
@@ -299,7 +341,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                     scale2(unbias(__byte_perm(uy, 0x64646464u, 0x4342)), k1)};
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma16816(hf ? su[nt] : st[nt], af, qf[nt][8 * hf + 2 * j], qf[nt][8 * hf + 2 * j + 1]);
+              mma16816(hf ? su[nt] : st[nt], af, qf[kBig ? 0 : nt][8 * hf + 2 * j], qf[kBig ? 0 : nt][8 * hf + 2 * j + 1]);
           }
         }
         // scores in log2 units; keys behind the sequence and nodes off the
@@ -473,7 +515,9 @@ cudaError_t launch_tree_few(const TreeArgs &a, cudaStream_t stream) {
   CUtensorMap tk, tv;
   if (!encode_codes(&tk, a.p.k_codes, rows, a.p.page_size) || !encode_codes(&tv, a.p.v_codes, rows, a.p.page_size))
     return cudaErrorInvalidValue;
-  return a.item_rows == 8 ? serve::launch<1>(tk, tv, a, stream) : serve::launch<2>(tk, tv, a, stream);
+  return a.item_rows == 8    ? serve::launch<1>(tk, tv, a, stream)
+         : a.item_rows == 16 ? serve::launch<2>(tk, tv, a, stream)
+                             : serve::launch<4>(tk, tv, a, stream);
 }
 
 }  // namespace h3kv

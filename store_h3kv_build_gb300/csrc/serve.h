@@ -78,7 +78,7 @@ struct TreeArgs {
 };
 size_t tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs);
 cudaError_t launch_attend_tree(const TreeArgs &a, cudaStream_t stream);
-// Its kernel for a.item_rows 8 or 16 (launch_attend_tree adds the join).
+// Its kernel for a.item_rows 8, 16 or 32 (launch_attend_tree adds the join).
 cudaError_t launch_tree_few(const TreeArgs &a, cudaStream_t stream);
 // 2-D map over 8-bit codes [rows, 128]: box 128 x box_rows, 128-byte swizzle.
 bool encode_codes(CUtensorMap *m, const void *base, int64_t rows, uint32_t box_rows);

@@ -20,7 +20,7 @@ namespace {
 constexpr int kMaxCtas = 152;
 
 // Rows of an item (a row tile of one sequence and kv head): 256 on the tcgen05
-// pipeline, 8 or 16 on the few-row kernel.
+// pipeline, 8, 16 or 32 on the few-row kernel.
 constexpr int kManyRows = 256;
 
 // Which of them, by the mean rows of a sequence and kv head (the host does not
@@ -28,11 +28,12 @@ constexpr int kManyRows = 256;
 // 32 x 8192, 1 x 32768 and 128 x 1024 cached tokens, 8 kv heads, 4 query heads
 // each: 8 rows 95, 20 and 62 us in items of 8, 123, 24 and 83 in items of 16; 16
 // rows 124, 26 and 87 us in items of 16, 176, 30 and 111 in two of 8; 32 rows
-// 234, 38 and 162 us in two items of 16, 236, 43 and 215 on the pipeline; 40 rows
-// 342, 50 and 235 us in three items of 16, 239, 43 and 221 on the pipeline.
+// 161, 37 and 128 us in items of 32, 234, 38 and 162 in two of 16, 236, 43 and
+// 215 on the pipeline; 40 rows 239, 43 and 221 us on the pipeline, 342, 50 and
+// 235 in three items of 16 (and two of 32 would take twice the 161).
 inline int item_rows_of(int32_t group, int64_t nodes, int32_t seqs) {
   const int64_t mean = (group * nodes + seqs - 1) / (seqs > 0 ? seqs : 1);
-  return mean <= 8 ? 8 : mean <= 32 ? 16 : kManyRows;
+  return mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 ? 32 : kManyRows;
 }
 
 // An item that lies on several CTAs, as the second of them describes it to the
@@ -72,8 +73,9 @@ __device__ inline Workspace workspace_of(const TreeArgs &a) {
 // 80, 80 and 83 us at 2, 3, 4 and 6 tiles (one token each: items of 8 rows), 139,
 // 118, 104 and 106 (4 nodes: items of 16), and 243, 218 and 220 us at 4, 6 and 8
 // (64 nodes).  100 of 64 .. 8192: 102, 86, 88 and 93; 161, 129, 116 and 121; 278,
-// 268 and 280.
-inline int item_cost_of(int32_t item_rows) { return item_rows == kManyRows ? 6 : item_rows == 16 ? 4 : 3; }
+// 268 and 280.  Items of 32 (8 nodes) at 4, 5 and 7: 154, 142 and 145; 170, 159 and
+// 162.
+inline int item_cost_of(int32_t item_rows) { return item_rows == kManyRows ? 6 : item_rows == 32 ? 5 : item_rows == 16 ? 4 : 3; }
 
 // A sequence's counts; tiles == 0: nothing to do (empty, or out of range).
 struct Counts {

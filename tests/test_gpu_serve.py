@@ -526,7 +526,7 @@ def test_tree_many_sequences_of_many_rows(cuda):
 
 @pytest.mark.parametrize("hq,hk", [(4, 1), (32, 1), (19, 1), (8, 2)])
 def test_tree_between_few_and_many_rows(cuda, hq, hk):
-    # a mean of 17 to 32 rows a sequence and kv head: items of 16 rows, some
+    # a mean of 17 to 32 rows a sequence and kv head: items of 32 rows, some
     # sequences with many of them
     g = np.random.default_rng(hq)
     n = 40 if hq < 16 else 12
@@ -787,13 +787,13 @@ def test_withheld_arrivals_run_into_the_wait_limit(cuda):
     st, _ = random_store(40, 8, 128)
     t = i32_2d([list(range(40))])
     q = normal(1, 8, 1500, 128).to(DEV)
-    qt = {n: normal(2, 64, n, 128).to(DEV) for n in (1, 2, 40)}
+    qt = {n: normal(2, 64, n, 128).to(DEV) for n in (1, 2, 4, 40)}
     calls = [lambda: b.attend_prompt(q, q, q, i32([0, 1500])),
              lambda: b.attend_tree(qt[40], st, t, i32([5000]), i32([0, 40]))]
     # the kernels for few rows wait for a freed stage, which takes more tiles
     # than stages on a CTA: many sequences over the same pages
     many = 24
-    for n in (1, 2):
+    for n in (1, 2, 4):
         qm = qt[n].repeat(1, many, 1)
         calls.append(lambda qm=qm, n=n: b.attend_tree(qm, st, t.expand(many, 40).contiguous(), i32([5000] * many),
                                                       i32(range(0, many * n + 1, n))))
