@@ -43,7 +43,7 @@ using attn::kTileBytes;
 using attn::warp_wait;
 
 // Register split per warpgroup, sums to 512 = 4 x 128 (the launch's share).
-constexpr uint32_t kRegSoftmax = 184, kRegDequant = 72, kRegIssue = 72;
+constexpr uint32_t kRegSoftmax = 184, kRegDequant = 80, kRegIssue = 64;
 static_assert(2 * kRegSoftmax + kRegDequant + kRegIssue == 512, "register split");
 
 // Stands for "no key yet" in a running maximum: finite, so that no difference
