@@ -348,15 +348,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && go) mbar_arrive(smem_u32(&sm.last_copies));
         __syncwarp();
       }
-      if (sm.abort) {
-        // every copy this thread issued must land before the CTA exits
-        for (int q = 0; q < 2; ++q)
-          if (q_issued[q]) mbar_wait_drain(smem_u32(&sm.q_full[q]), (q_issued[q] - 1) & 1, kDrainNs);
-        for (int x = 0; x < kNK; ++x)
-          if (k_issued[x]) mbar_wait_drain(smem_u32(&sm.k_load[x]), (k_issued[x] - 1) & 1, kDrainNs);
-        for (int x = 0; x < kNV; ++x)
-          if (v_issued[x]) mbar_wait_drain(smem_u32(&sm.v_load[x]), (v_issued[x] - 1) & 1, kDrainNs);
-      }
+      // every copy this thread issued must land before the CTA exits, also
+      // where another warp gives up behind the last of them
+      for (int q = 0; q < 2; ++q)
+        if (q_issued[q]) mbar_wait_drain(smem_u32(&sm.q_full[q]), (q_issued[q] - 1) & 1, kDrainNs);
+      for (int x = 0; x < kNK; ++x)
+        if (k_issued[x]) mbar_wait_drain(smem_u32(&sm.k_load[x]), (k_issued[x] - 1) & 1, kDrainNs);
+      for (int x = 0; x < kNV; ++x)
+        if (v_issued[x]) mbar_wait_drain(smem_u32(&sm.v_load[x]), (v_issued[x] - 1) & 1, kDrainNs);
     } else if (warp == 13) {
       // ====================================================== MMA issuer
       MmaState m;

@@ -65,11 +65,10 @@ __device__ __forceinline__ void produce(const TreeArgs &a, TreeSmem &sm, uint8_t
       r.next();
     }
   }
-  if (sm.abort) {
-    // every copy that was issued must land before the CTA exits
-    for (int x = 0; x < kDepth; ++x)
-      if (issued[x]) mbar_wait_drain(smem_u32(&load[x]), (issued[x] - 1) & 1, kDrainNs);
-  }
+  // every copy that was issued must land before the CTA exits, also where
+  // another warp gives up behind the last of them
+  for (int x = 0; x < kDepth; ++x)
+    if (issued[x]) mbar_wait_drain(smem_u32(&load[x]), (issued[x] - 1) & 1, kDrainNs);
 }
 
 // q' = fp16(q H) of 32 rows of a segment, from row w0 on, into rows t0 .. of the

@@ -207,11 +207,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         r.next();
       }
     }
-    if (sm.abort) {
-      // every copy that was issued must land before the CTA exits
-      for (int x = 0; x < kStages; ++x)
-        if (issued[x]) mbar_wait_drain(smem_u32(&sm.full[x]), (issued[x] - 1) & 1, kDrainNs);
-    }
+    // every copy that was issued must land before the CTA exits, also where a
+    // consumer gives up behind the last of them
+    for (int x = 0; x < kStages; ++x)
+      if (issued[x]) mbar_wait_drain(smem_u32(&sm.full[x]), (issued[x] - 1) & 1, kDrainNs);
     return;
   }
 

@@ -127,11 +127,10 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
         phase ^= 1u;
       }
     }
-    if (sm.abort) {
-      // every copy that was issued must land before the CTA exits
-      for (int s = 0; s < kAppendStages; ++s)
-        if (issued[s]) mbar_wait_drain(smem_u32(&sm.full[s]), (issued[s] - 1) & 1, kDrainNs);
-    }
+    // every copy that was issued must land before the CTA exits, also where a
+    // row warp gives up behind the last of them
+    for (int s = 0; s < kAppendStages; ++s)
+      if (issued[s]) mbar_wait_drain(smem_u32(&sm.full[s]), (issued[s] - 1) & 1, kDrainNs);
     return;
   }
   const int i = tid >> 1, hf = tid & 1;  // row in the tile, half of the result
