@@ -122,8 +122,11 @@ h3kv_status h3kv_attend_tree(const h3kv_rows *Q, int32_t q_heads, int64_t nodes,
  * behind its prefix; otherwise every row sees every key of its sequence.
  *   S = Q K^T softmax_scale; O = bf16(softmax(S) V), P rounded to bf16 for
  *   the second product, fp32 accumulation; lse as above, or NULL.
- * A row that sees no key gets O = 0 and lse = -infinity.  A value of K or V
- * that is infinite or NaN reaches no row of another sequence. */
+ * Scores are held in fp32 and may have any size that fp32 holds; a row with one
+ * of +infinity is undefined.  A row that sees no key (or only scores of
+ * -infinity) gets O = 0 and lse = -infinity.  A value of K or V that is infinite
+ * or NaN reaches no row of another sequence; within its own it may reach rows
+ * that do not see it (a weight of 0 times such a value of V). */
 h3kv_status h3kv_attend_prompt(const h3kv_rows *Q, int32_t q_heads, int64_t q_rows, const h3kv_rows *K,
                                const h3kv_rows *V, int32_t kv_heads, int64_t k_rows, const int32_t *cu_q,
                                const int32_t *cu_k, int32_t seqs, int32_t causal, float softmax_scale,

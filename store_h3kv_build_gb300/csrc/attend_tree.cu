@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kJoinWarpsFew * 32) join_kernel(const TreeArgs
 #pragma unroll
   for (int e = 0; e < 16; ++e) o[e] = 0.f;
   auto add = [&](float2 ml, const float (&p)[16]) {
-    const float mn = fmaxf(m, ml.x), ga = ex2((m - mn) * c2), gb = ex2((ml.x - mn) * c2);
+    const float mn = fmaxf(m, ml.x), ref = mn == kNoMax ? 0.f : mn;
+    const float ga = ex2((m - ref) * c2), gb = ex2((ml.x - ref) * c2);
     l = fmaf(l, ga, ml.y * gb);
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = fmaf(o[e], ga, p[e] * gb);

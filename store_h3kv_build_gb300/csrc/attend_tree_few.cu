@@ -35,6 +35,9 @@ constexpr int kFewThreads = (kWarps + kProducers + 1) * 32;
 constexpr int kCodeBytes = kBN * 128;      // one tile's codes
 constexpr int kPitch = 132;                // floats of a row in the join buffer
 constexpr int kQPitch = 136;               // values of a query row: 16 bytes aside, so that 8 rows' reads spread
+// "No key yet" in a running maximum, which is in log2 units here: finite, so
+// that no difference of two infinities arises, and no score is below it.
+constexpr float kNoMaxLog2 = -3.4e38f;
 
 template <int kNT>
 struct FewSmem {
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int t = 0; t < 8; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
-      m[nt][0] = m[nt][1] = kNoMax;
+      m[nt][0] = m[nt][1] = kNoMaxLog2;
       l[nt][0] = l[nt][1] = 0.f;
     }
     const int32_t keys = static_cast<int32_t>(s.keys);

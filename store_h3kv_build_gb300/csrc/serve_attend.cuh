@@ -46,10 +46,14 @@ using attn::warp_wait;
 constexpr uint32_t kRegSoftmax = 184, kRegDequant = 80, kRegIssue = 64;
 static_assert(2 * kRegSoftmax + kRegDequant + kRegIssue == 512, "register split");
 
-// Stands for "no key yet" in a running maximum: finite, so that no difference
-// of two infinities arises, and below any score of bf16 or fp16 operands that
-// has a weight at all.
-constexpr float kNoMax = -1e30f;
+// "No key yet" in a running maximum.  (Not a low finite value: bf16 operands
+// reach any score that fp32 holds.)
+constexpr float kNoMax = -INFINITY;
+// Up to this |maximum| of a tile in log2 units a weight is ex2(s c2 - m c2) with
+// m c2 rounded to fp32: the rounding, at most 2^-9, is common to the weights
+// that are relative to m.  Beyond, where it would grow to whole powers of two,
+// m is subtracted from the scores before the product.
+constexpr float kFusedMaxLog2 = 65536.f;
 
 struct Smem {
   uint8_t q[2][kTileBytes];
@@ -306,21 +310,39 @@ __device__ __forceinline__ void mask_tile(uint32_t tS, const uint32_t (&see)[4])
   tmem_wait_st();
 }
 
+// Subtracts `ref` from a tile's scores in TMEM, a loop like mask_tile.
+__device__ __forceinline__ void shift_tile(uint32_t tS, float ref) {
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint32_t x[32];
+    tmem_ld32(tS + 32 * g, x);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) - ref);
+    tmem_st32(tS + 32 * g, x);
+  }
+  tmem_wait_st();
+}
+
 // One 128-key tile: S from TMEM, running maximum, P back to TMEM.
 template <bool kF16>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, float c2, Row &r) {
   float s[128];
   float m4[4];
   tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
-  const float mt = fmaxf(fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])), kNoMax);
+  const float mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
   if (first) {
     r.m = mt;
     r.l = 0.f;
-  } else {
-    // O is rescaled only when the maximum grows by more than 2^8 (exact: the
-    // weights are relative to r.m, whatever it is)
-    const bool need = (mt - r.m) * c2 > kLazyRescaleLog2;
-    if (__any_sync(0xffffffffu, need)) {
+  }
+  // O is rescaled only when the maximum grows by more than 2^8 (exact: the
+  // weights are relative to r.m, whatever it is); infinite differences from and
+  // to kNoMax give a factor of 0 and no growth.  The two rare cases share one
+  // vote: with a vote of its own for `far`, 40 prompts of 300 tokens took 87 us,
+  // 79 so and without.
+  const bool need = (mt - r.m) * c2 > kLazyRescaleLog2, far = fabsf(mt) * c2 > kFusedMaxLog2 && mt != kNoMax;
+  float cm = c2;
+  if (__any_sync(0xffffffffu, need || far)) {
+    if (!first) {
       const float alpha = need ? ex2((r.m - mt) * c2) : 1.f;
       if (need) {
         r.l *= alpha;
@@ -335,8 +357,14 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool firs
         tmem_st16(tO + c * 16, o);
       }
     }
+    if (__any_sync(0xffffffffu, far)) {
+      shift_tile(tS, r.m == kNoMax ? 0.f : r.m);
+      tmem_ld128_max(tS, *reinterpret_cast<uint32_t(*)[128]>(s), m4);
+      cm = 0.f;
+    }
   }
-  const float2 cc = make_float2(c2, c2), nm = make_float2(-r.m * c2, -r.m * c2);
+  const float bias = r.m == kNoMax ? 0.f : -r.m * cm;  // (kNoMax: all scores are -infinity)
+  const float2 cc = make_float2(c2, c2), nm = make_float2(bias, bias);
   float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -369,9 +397,9 @@ __device__ __forceinline__ void prefix_mask(int32_t n, uint32_t (&see)[4]) {
 
 // Joins stream 1's (max, sum) into r: the weights of the two streams' O.
 __device__ __forceinline__ void join_rows(Row &r, float2 other, float c2, float &ga, float &gb) {
-  const float m = fmaxf(r.m, other.x);
-  ga = ex2((r.m - m) * c2);
-  gb = ex2((other.x - m) * c2);
+  const float m = fmaxf(r.m, other.x), ref = m == kNoMax ? 0.f : m;
+  ga = ex2((r.m - ref) * c2);
+  gb = ex2((other.x - ref) * c2);
   r.l = fmaf(r.l, ga, other.y * gb);
   r.m = m;
 }
