@@ -102,7 +102,8 @@ size_t h3kv_attend_tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64
  * same sequence; any other value (-1, say) makes the node a root.  parents
  * NULL: node j's parent is j - 1, a plain run of tokens.
  *   q' = fp16(Q H), K' = fp16(code * scale), V' likewise;
- *   S = q' K'^T softmax_scale;  O = bf16((softmax(S) V') H);
+ *   S = q' K'^T softmax_scale;  O = bf16((softmax(S) V') H), weights rounded to
+ *   fp16 for the second product (down to 2^-32 of the largest), fp32 sums;
  *   lse = ln(sum exp S), fp32 [q_heads, nodes] contiguous, or NULL.
  * softmax_scale <= 0 selects 1/sqrt(128).  nodes: the rows of Q.
  * q_heads / kv_heads is at most 64.  The keys of a sequence are split over

@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       const End e = ok ? fin.at_end(sm, s, q, warp_on, row, c2, &joined, &ga, &gb, w) : kFailed;
       if (e == kFailed) break;
       if (e == kWrite) {
+        // (without the weights' factor)
+        row.l *= kWeightInv;
+        ga *= kWeightInv;
+        gb *= kWeightInv;
         const bool live = r < s.rows;
         if (s.whole) {
           // H128 = [[H64, H64], [H64, -H64]]: the output's halves are the

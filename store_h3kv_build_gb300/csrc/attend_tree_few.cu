@@ -252,7 +252,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     const int32_t base_key = static_cast<int32_t>(s.keys) - s.nodes;
     float o[kNT][8][4];
-    float m[kNT][2], l[kNT][2];  // of rows 8 nt + 2 i4 + {0, 1}; m in log2 units
+    // of rows 8 nt + 2 i4 + {0, 1}: what the weights are relative to, in log2
+    // units (the maximum when it was set, less kWeightLog2), and their sum
+    float m[kNT][2], l[kNT][2];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) grow |= fmaxf(st[nt][e], st[nt][2 + e]) - m[nt][e] > kLazyRescaleLog2;
+          for (int e = 0; e < 2; ++e) grow |= fmaxf(st[nt][e], st[nt][2 + e]) - m[nt][e] > kLazyRescaleLog2 + kWeightLog2;
         }
         // the maximum follows only when a score passes it by more than 2^8
         if (__any_sync(0xffffffffu, grow)) {
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              x = fmaxf(x, m[nt][e]);
+              x = fmaxf(x - kWeightLog2, m[nt][e]);
               const float al = ex2(m[nt][e] - x);
               m[nt][e] = x;
               l[nt][e] *= al;

@@ -55,6 +55,12 @@ constexpr float kNoMax = -INFINITY;
 // m is subtracted from the scores before the product.
 constexpr float kFusedMaxLog2 = 65536.f;
 
+// fp16 weights carry a factor of 2^7: relative to a maximum that may have grown
+// by 2^8 they stay below 2^15, and what fp16 cannot hold lies below 2^-32 of the
+// maximum (an error of 2^-12 over a million keys; 2^-5 without the factor, where
+// weights of 2^-25 were lost).  bf16 weights need none.
+constexpr float kWeightLog2 = 7.f, kWeightInv = 0.0078125f;
+
 struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kNK][kTileBytes];
@@ -363,7 +369,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool firs
       cm = 0.f;
     }
   }
-  const float bias = r.m == kNoMax ? 0.f : -r.m * cm;  // (kNoMax: all scores are -infinity)
+  constexpr float kUp = kF16 ? kWeightLog2 : 0.f;
+  const float bias = r.m == kNoMax ? kUp : fmaf(-r.m, cm, kUp);  // (kNoMax: all scores are -infinity)
   const float2 cc = make_float2(c2, c2), nm = make_float2(bias, bias);
   float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll

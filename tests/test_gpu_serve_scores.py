@@ -160,3 +160,35 @@ def test_tree_scores_of_any_size(cuda, hq, m, scale, n):
     for h in range(hq):
         close(out[h], o[h // (hq // hk)], off[h // (hq // hk)], f"{n} rows, head {h}")
     check_lse(lse, np.broadcast_to(score, (hq, m)), see.sum(1)[None], f"{n} rows lse")
+
+
+@pytest.mark.parametrize("hq,m", [(1, 1), (8, 2), (8, 4), (8, 8)])
+@pytest.mark.parametrize("x", [20.3, 24.6, 25.5, 28.0])
+def test_tree_many_small_weights_beside_a_large_one(cuda, hq, m, x):
+    """A million cached rows, each 2^-x of the weight of one: together as much
+    as 2^20 2^-x.  fp16 holds a weight to half a step (2^-11 of it), or to 2^-32
+    of the largest where it is subnormal.  As many sequences (over the same
+    pages) as there are SMs, so that no split of the keys separates them."""
+    seqs = torch.cuda.get_device_properties(0).multi_processor_count
+    n, ps = 1 << 20, 128
+    pages = n // ps
+    st = b.PagedStore(*(torch.zeros((pages, 1, ps, 128), dtype=torch.int8, device=DEV) for _ in range(2)),
+                      *(torch.zeros((pages, 1, ps), dtype=torch.float16, device=DEV) for _ in range(2)))
+    st.k_codes[5, 0, 77, 0], st.k_scales[5, 0, 77] = 127, 1 / 64
+    st.v_codes[..., 0], st.v_scales[:] = 100, 1 / 64
+    st.v_codes[5, 0, 77] = 0
+    q = torch.full((hq, seqs * m, 128), 3.0, dtype=torch.bfloat16)
+    qr = oracle.fp16_round(oracle.rotate(oracle.as_f64(q)))[0, 0]
+    score = qr[0] * 127 / 64
+    assert (qr[1:] == 0).all()
+    scale = float(np.float32(x * np.log(2.0) / score))
+    parents = torch.full((seqs * m,), -1, dtype=torch.int32, device=DEV)  # every node beside the others
+    out = b.attend_tree(q.to(DEV), st, i32([list(range(pages))] * seqs), i32([n] * seqs),
+                        i32(list(range(0, seqs * m + 1, m))), parents, softmax_scale=scale)
+    b.sync_status()
+    rest = (n - m) * np.exp(-score * scale)  # n - m keys before, and itself
+    want = rest / (1 + rest) * (100 / 64) / np.sqrt(128.0)
+    w = np.exp2(-x)
+    # the score's fp32 roundings move a weight by 2^-20 of it; sums as above
+    off = want * (2.0 ** -11 + 2.0 ** -18 + 2.0 ** -8) + (n - m) * min(2.0 ** -32, w) / (1 + rest) * (100 / 64) / np.sqrt(128.0)
+    close(out, np.full((hq, seqs * m, 128), want), off, f"x {x}")
