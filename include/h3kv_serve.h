@@ -58,7 +58,8 @@ size_t h3kv_paged_store_bytes(int32_t pages, int32_t kv_heads, int32_t page_size
 
 /* Rotate and quantise the n rows of K and V (bf16 [kv_heads, n, 128]) and
  * write row i to pool row rows[i]; a negative rows[i] leaves the row out.  No
- * pool row may be named twice in one call. */
+ * pool row may be named twice in one call.  A row that holds a NaN gets a scale
+ * of NaN: it reads back as NaN, and so does what attends to it. */
 h3kv_status h3kv_paged_append(const h3kv_rows *K, const h3kv_rows *V, const int32_t *rows, int64_t n,
                               const h3kv_paged_store *store, void *stream);
 
@@ -106,6 +107,9 @@ size_t h3kv_attend_tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64
  *   fp16 for the second product (down to 2^-32 of the largest), fp32 sums;
  *   lse = ln(sum exp S), fp32 [q_heads, nodes] contiguous, or NULL.
  * softmax_scale <= 0 selects 1/sqrt(128).  nodes: the rows of Q.
+ * A cached row that is not finite (a scale of NaN, or code * scale beyond fp16)
+ * may reach every node of its own sequence, also those that do not see it, and
+ * none of another's.
  * q_heads / kv_heads is at most 64.  The keys of a sequence are split over
  * the GPU's SMs and joined by their log-sum-exp in a fixed order: the same
  * call gives the same bits, another batch around a sequence may round

@@ -178,6 +178,9 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     if ((bits & 0x1FFFu) == 0x1000u) scale = __uint_as_float(bits + (e > 0.f ? 1 : e < 0.f ? -1 : 0));
     __half s = __float2half_rn(scale);
     if (__hisinf(s)) s = __ushort_as_half(0x7BFFu);
+    // the maximum drops NaN: a row that holds one (every transformed value is
+    // NaN then) says so by its scale
+    if (x[0] != x[0]) s = __ushort_as_half(0x7FFFu);
     const float sf = __half2float(s);
     const float m = sf > 0.f ? kInvSqrt128 * 128.0f / sf : 0.f;
     if (r >= 0) {

@@ -1,0 +1,64 @@
+"""The paged cache where its rows are unusual: NaN, infinities, subnormal scales
+and few rows at a time."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from store_h3kv_build_gb300 import binding as b
+from store_h3kv_build_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def normal(seed, *shape):
+    return synth.normal_f32(shape, seed).to(torch.bfloat16)
+
+
+def empty_store(pages, heads, ps, fill=5):
+    st = b.PagedStore.empty(pages, heads, ps)
+    for t in st.tensors().values():
+        t.fill_(fill)
+    return st
+
+
+@pytest.mark.parametrize("n", [1, 7, 300])
+def test_rows_that_hold_a_nan_read_back_as_nan(cuda, n):
+    heads, ps = 2, 32
+    k, v = normal(1, heads, n, 128), normal(2, heads, n, 128)
+    bad = list(range(0, n, 3))
+    for j, i in enumerate(bad):
+        k[j % 2, i, (37 * j) % 128] = float("nan")
+        v[1 - j % 2, i] = float("nan")
+    pages = -(-n // ps)
+    st = empty_store(pages, heads, ps)
+    b.paged_append(k.to(DEV), v.to(DEV), st, torch.arange(n, dtype=torch.int32, device=DEV))
+    rk, rv = b.paged_read(st, torch.arange(n, dtype=torch.int32, device=DEV))
+    b.sync_status()
+    for x, back in ((k, rk.cpu()), (v, rv.cpu())):
+        nan = x.isnan().any(-1)
+        assert back[nan].isnan().all() and not back[~nan].isnan().any()
+        # half a code of the row's scale in each of 128 rotated values, and bf16
+        ref = x.float()[~nan]
+        scale = torch.from_numpy(oracle.encode_rows(x.nan_to_num(0.0))[1]).float()[~nan]
+        off = 0.6 * scale[:, None] * 128 ** 0.5 + 2.0 ** -8 * ref.abs() + 1e-6
+        assert ((back.float()[~nan] - ref).abs() <= off).all()
+
+
+@pytest.mark.parametrize("nodes,hq", [(1, 2), (8, 4), (40, 8)])
+def test_attention_over_a_nan_row_is_nan(cuda, nodes, hq):
+    # and another sequence's is not
+    heads, ps, n = 2, 32, 200
+    k, v = normal(1, heads, 2 * 224, 128), normal(2, heads, 2 * 224, 128)
+    k[:, 70, 3] = float("nan")
+    st = empty_store(14, heads, ps)
+    b.paged_append(k.to(DEV), v.to(DEV), st, torch.arange(448, dtype=torch.int32, device=DEV))
+    q = normal(3, hq, 2 * nodes, 128)
+    out = b.attend_tree(q.to(DEV), st, i32([list(range(7)), list(range(7, 14))]), i32([n, n]), i32([0, nodes, 2 * nodes]))
+    b.sync_status()
+    assert out[:, :nodes].isnan().all() and out[:, nodes:].isfinite().all()
