@@ -171,11 +171,15 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     // s = fp16(absmax(x H) / 127), saturated; codes rne(x H / s) with the stored
     // s.  absmax * sqrt(128) / 127 in two fp32 parts p + e: where p alone lies
     // on the tie between two fp16 values, e says which side the product is on.
+    // On a tie the bits that fp16 drops (13, and one more for each power of two
+    // below its least normal value 2^-14) are a one and zeros.
     constexpr float kHi = 0.08908431977033615f, kLo = -8.806923523785315e-10f;  // sqrt(128) / 127
     float scale = a * kHi;
     const float e = fmaf(a, kLo, fmaf(a, kHi, -scale));
     const uint32_t bits = __float_as_uint(scale);
-    if ((bits & 0x1FFFu) == 0x1000u) scale = __uint_as_float(bits + (e > 0.f ? 1 : e < 0.f ? -1 : 0));
+    const int kept = min(19, static_cast<int>(bits >> 23) - 94);
+    if (kept >= 8 && ((bits & 0x7FFFFFu) | 0x800000u) << kept == 0x80000000u)
+      scale = __uint_as_float(bits + (e > 0.f ? 1 : e < 0.f ? -1 : 0));
     __half s = __float2half_rn(scale);
     if (__hisinf(s)) s = __ushort_as_half(0x7BFFu);
     // the maximum drops NaN: a row that holds one (every transformed value is

@@ -62,3 +62,20 @@ def test_attention_over_a_nan_row_is_nan(cuda, nodes, hq):
     out = b.attend_tree(q.to(DEV), st, i32([list(range(7)), list(range(7, 14))]), i32([n, n]), i32([0, nodes, 2 * nodes]))
     b.sync_status()
     assert out[:, :nodes].isnan().all() and out[:, nodes:].isfinite().all()
+
+
+@pytest.mark.parametrize("pair", [(0.000469207763671875, 1.8253922462463379e-06), (0.023193359375, 0.00022983551025390625),
+                                  (0.0233154296875, 0.00010776519775390625)])
+def test_subnormal_scales_next_to_a_tie(cuda, pair):
+    # (v1 + v2) / (sqrt(128) 127) rounds to an fp32 value halfway between two
+    # subnormal fp16 ones, and lies 5e-8 or 2e-8 of itself below that: fp64
+    # tells the side
+    k = torch.zeros((1, 1, 128), dtype=torch.bfloat16)
+    k[0, 0, 0], k[0, 0, 1] = pair
+    assert tuple(k[0, 0, :2].tolist()) == pair
+    st = empty_store(1, 1, 16)
+    b.paged_append(k.to(DEV), -k.to(DEV), st, i32([3]))
+    b.sync_status()
+    want = oracle.encode_rows(k)[1].item()
+    assert 0 < want < 2 ** -14
+    assert st.k_scales[0, 0, 3].item() == want and st.v_scales[0, 0, 3].item() == want
