@@ -79,3 +79,28 @@ def test_subnormal_scales_next_to_a_tie(cuda, pair):
     want = oracle.encode_rows(k)[1].item()
     assert 0 < want < 2 ** -14
     assert st.k_scales[0, 0, 3].item() == want and st.v_scales[0, 0, 3].item() == want
+
+
+@pytest.mark.parametrize("heads,n", [(1, 1), (2, 3), (8, 16)])
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-5, 3e3])
+def test_append_of_few_rows_writes_the_scales(cuda, heads, n, size):
+    # rows without zeros, scales to one fp16 step of the oracle's, codes to one
+    # of theirs under the stored scale; every other row stays as it was
+    ps = 16
+    k, v = (normal(s, heads, n, 128).mul_(size) for s in (10 + n, 20 + n))
+    st = empty_store(3, heads, ps)
+    rows = torch.randperm(3 * ps, generator=torch.Generator().manual_seed(n))[:n]
+    b.paged_append(k.to(DEV), v.to(DEV), st, rows.to(torch.int32).to(DEV))
+    b.sync_status()
+    for x, name in ((k, "k"), (v, "v")):
+        codes, scales = getattr(st, name + "_codes").cpu(), getattr(st, name + "_scales").cpu()
+        got = scales[rows // ps, :, rows % ps].T.double().numpy()
+        want = oracle.encode_rows(x)[1]
+        step = np.spacing(want.astype(np.float16)).astype(np.float64)
+        assert (want > 0).all() and (np.abs(got - want) <= step).all()
+        ref = oracle.quantize(oracle.rotate(x), got)
+        assert np.abs(codes[rows // ps, :, rows % ps].transpose(0, 1).numpy().astype(int) - ref).max() <= 1
+        rest = torch.ones(3 * ps, dtype=torch.bool)
+        rest[rows] = False
+        rest = rest.view(3, ps)
+        assert (codes.transpose(1, 2)[rest] == 5).all() and (scales.transpose(1, 2)[rest] == 5).all()
