@@ -39,8 +39,10 @@ typedef struct {
 } h3kv_rows;
 
 /* A kvi8r cache in pages of page_size tokens (16, 32, 64 or 128).  Codes and
- * scales of a row are those of h3kv_build_store with one scale per row.  Row
- * number r of the pool is slot r % page_size of page r / page_size. */
+ * scales of a row have the format and the formula of h3kv_store with one scale
+ * per row.  h3kv_paged_append does not compute them as h3kv_build_store does:
+ * next to a rounding border a scale may differ by one fp16 step, a code by
+ * one.  Row number r of the pool is slot r % page_size of page r / page_size. */
 typedef struct {
   int8_t *k_codes;    /* [pages, kv_heads, page_size, 128] */
   int8_t *v_codes;

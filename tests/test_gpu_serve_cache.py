@@ -104,3 +104,25 @@ def test_append_of_few_rows_writes_the_scales(cuda, heads, n, size):
         rest[rows] = False
         rest = rest.view(3, ps)
         assert (codes.transpose(1, 2)[rest] == 5).all() and (scales.transpose(1, 2)[rest] == 5).all()
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-4])
+def test_append_beside_the_store_build(cuda, size):
+    """The pages hold the format of h3kv_build_store, whose scales and codes
+    may differ by a rounding: one fp16 step of a scale, one code."""
+    heads, n, ps = 4, 4096, 64
+    k, v = normal(1, heads, n, 128) * size, normal(2, heads, n, 128) * size
+    k[..., ::32] *= 20
+    whole = b.build_store(k.to(DEV), v.to(DEV))
+    st = b.PagedStore.empty(n // ps, heads, ps)
+    b.paged_append(k.to(DEV), v.to(DEV), st, torch.arange(n, dtype=torch.int32, device=DEV))
+    b.sync_status()
+    for name in ("k", "v"):
+        c = getattr(st, name + "_codes").transpose(0, 1).reshape(heads, n, 128).int()
+        s = getattr(st, name + "_scales").transpose(0, 1).reshape(heads, n)
+        c0, s0 = getattr(whole, name + "_codes").int(), getattr(whole, name + "_scales")
+        bits, bits0 = s.view(torch.int16).int(), s0.view(torch.int16).int()
+        assert (bits - bits0).abs().max() <= 1 and (bits != bits0).sum() <= 1e-3 * bits.numel()
+        same = bits == bits0
+        d = (c - c0).abs()[same]
+        assert d.max() <= 1 and (d != 0).sum() <= 1e-4 * d.numel()
