@@ -264,17 +264,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dealloc<kRegZero>();
     Ring<kNV> vr;
     uint32_t phase = 0;
+    int n = 0;
     bool ok = true;
-    while (ok && (ok = sr.get(sm.segs, w))) {
+    while (ok && (ok = sr.get(sm.segs, for_tiles(w, n)))) {
       const Seg &s = sr.seg(sm.segs);
-      const int n = s.n, rows = s.rows;
+      const int rows = s.rows;
+      n = s.n;
       const bool ragged = is_ragged(s);
       const int valid = static_cast<int>(s.keys - static_cast<int64_t>(n - 1) * kBN);
       sr.done(sm.segs);
       if (rows == 0) break;
       for (int t = 0; t < n; ++t) {
         if (ragged && t == n - 1) {
-          if (!(ok = warp_wait(smem_u32(&sm.v_tail), phase, w))) break;
+          if (!(ok = warp_wait(smem_u32(&sm.v_tail), phase, for_tiles(w, n)))) break;
           phase ^= 1u;
           const int r = (warp - 8) * 32 + lane;
           if (r >= valid) {
@@ -376,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<PromptSegs::kDepth> r;
       uint32_t block = blockIdx.x, phase = 0, copies_phase = 0;
       bool more = true;
+      int before = 0;  // key tiles of the segment before
       auto next_block = [&] {
         if (lane == 0) request_block(smem_u32(sm.taken), smem_u32(&sm.taken_bar));
         const bool came = warp_wait(smem_u32(&sm.taken_bar), phase, w);
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           more = next_block();  // (a block that no sequence needs)
         }
         if (!found) s.rows = s.n = 0;
-        if (!warp_wait(smem_u32(&sm.segs.empty[r.slot]), r.phase ^ 1u, w)) break;
+        if (!warp_wait(smem_u32(&sm.segs.empty[r.slot]), r.phase ^ 1u, for_tiles(w, before))) break;
         if (lane == 0) {
           sm.segs.seg[r.slot] = s;
           mbar_arrive(smem_u32(&sm.segs.full[r.slot]));
@@ -406,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // another block is asked for only when this segment's last copies are
         // under way (two tiles before its end): taken earlier, it would wait
         // here while other SMs run out of work
-        if (!warp_wait(smem_u32(&sm.last_copies), copies_phase, w)) break;
+        before = s.n;
+        if (!warp_wait(smem_u32(&sm.last_copies), copies_phase, for_tiles(w, s.n))) break;
         copies_phase ^= 1u;
         more = next_block();
       }

@@ -268,10 +268,13 @@ __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &
   walk.start(a, sc);
   Ring<TreeSegs::kDepth> r;
   bool described = false;
+  int last = 0, before = 0;  // key tiles of the last segment and the one before
   for (;;) {
     Seg s;
     const bool more = walk.next(a, &s);
-    if (!warp_wait(smem_u32(&ring.empty[r.slot]), r.phase ^ 1u, w)) return;
+    if (!warp_wait(smem_u32(&ring.empty[r.slot]), r.phase ^ 1u, for_tiles(w, last + before))) return;
+    before = last;
+    last = s.n;
     if ((threadIdx.x & 31) == 0) {
       ring.seg[r.slot] = s;
       mbar_arrive(smem_u32(&ring.full[r.slot]));

@@ -69,3 +69,33 @@ def test_calls_after_waits_that_all_gave_up(cuda):
         for x, y in zip(got, want):
             assert x is None or torch.equal(x, y)
         assert all(torch.equal(x, y) for x, y in zip(st.tensors().values(), before))
+
+
+def test_prompts_longer_than_the_limit(cuda):
+    """Warps that wait for a segment's end are not held to the limit of a
+    tile: 1024 key tiles of over a microsecond each, under a limit of 300."""
+    n = 131072
+    q, k, v = normal(1, 1, 300, 128), normal(2, 1, n, 128), normal(3, 1, n, 128)
+    for causal, cu in ((False, [0, 300]), (True, [0, 256]), (False, [0, 1, 300])):
+        keys = [0, n - 77] if len(cu) == 2 else [0, n // 2, n - 5]
+        want = b.attend_prompt(q, k, v, i32(cu), i32(keys), causal=causal)[:, :cu[-1]]
+        with limit(300_000):
+            got = b.attend_prompt(q, k, v, i32(cu), i32(keys), causal=causal)[:, :cu[-1]]
+            b.sync_status()
+        assert torch.equal(got, want)
+
+
+def test_trees_longer_than_the_limit(cuda):
+    """The same for the cache: several long items on each CTA."""
+    hk, ps, n = 8, 128, 65536
+    st = b.PagedStore.empty(n // ps, hk, ps, device=DEV)
+    b.paged_append(normal(1, hk, n, 128), normal(2, hk, n, 128), st, torch.arange(n, dtype=torch.int32, device=DEV))
+    seqs = 29  # 232 items, 152 CTAs
+    table, lens = i32([list(range(n // ps))] * seqs), i32([n] * seqs)
+    for m, hq in ((1, 64), (2, 64), (4, 64), (8, 64)):
+        q, cu = normal(3 + m, hq, seqs * m, 128), i32(list(range(0, seqs * m + 1, m)))
+        want = b.attend_tree(q, st, table, lens, cu)
+        with limit(100_000):
+            got = b.attend_tree(q, st, table, lens, cu)
+            b.sync_status()
+        assert torch.equal(got, want)
