@@ -19,6 +19,10 @@
  *  - Packed tensors: the rows cu[i] .. cu[i+1]-1 belong to sequence i.  Rows
  *    before cu[0] and from cu[seqs] on belong to none; nothing is written for
  *    them.
+ *  - What a call writes shares no memory with what else it reads or writes:
+ *    H3KV_ERR_INVALID_ARG, by the tensors' extents.  K and V of a read may take
+ *    turns in one buffer (equal strides), and O of the attention calls may lie
+ *    beside Q, K and V in one; O is not compared with those.
  *  - H3KV_OK for empty work (no rows, no sequences), with nothing launched.
  */
 #ifndef H3KV_SERVE_H

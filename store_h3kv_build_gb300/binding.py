@@ -544,6 +544,17 @@ def _need_apart(out, **inputs) -> None:
             raise ValueError(f"out: shares memory with {name}")
 
 
+def _check_apart(status: int, where: str, outs: dict, ins: dict) -> None:
+    """check() of a call that refuses outputs over its inputs or over one
+    another; says which where that is why."""
+    if status == H3KV_ERR_INVALID_ARG:
+        outs = {n: t for n, t in outs.items() if t is not None}
+        for i, t in enumerate(outs.values()):
+            others = {"another output" if n == "out" else n: x for n, x in list(outs.items())[:i]}
+            _need_apart(t, **ins, **others)
+    check(status, where)
+
+
 def _one_device(stream, first, *others) -> int:
     """The index of the CUDA device that every tensor of a call (and the
     stream) is on."""
@@ -651,8 +662,9 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, store: PagedStore, rows: torc
     dev = _one_device(stream, K, V, rows, store._buffers[0])
     if _current_device() != dev:
         return _on_device(dev, paged_append, K, V, store, rows, stream)
-    check(h3kv_paged_append(ctypes.byref(k), ctypes.byref(v), rows.data_ptr(), n, store._ref, _handle(dev, stream)),
-          "h3kv_paged_append")
+    st = h3kv_paged_append(ctypes.byref(k), ctypes.byref(v), rows.data_ptr(), n, store._ref, _handle(dev, stream))
+    if st != H3KV_OK:
+        _check_apart(st, "h3kv_paged_append", store.tensors(), dict(K=K, V=V, rows=rows))
 
 
 def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = None, V: torch.Tensor | None = None,
@@ -678,8 +690,9 @@ def paged_read(store: PagedStore, rows: torch.Tensor, K: torch.Tensor | None = N
         _need_apart(V, rows=rows, **store.tensors())
     if k.data == v.data and n and store.kv_heads:
         raise ValueError("out: K shares memory with V")
-    check(h3kv_paged_read(store._ref, rows.data_ptr(), n, ctypes.byref(k), ctypes.byref(v), _handle(dev, stream)),
-          "h3kv_paged_read")
+    st = h3kv_paged_read(store._ref, rows.data_ptr(), n, ctypes.byref(k), ctypes.byref(v), _handle(dev, stream))
+    if st != H3KV_OK:
+        _check_apart(st, "h3kv_paged_read", dict(K=K, V=V), {})
     return K, V
 
 
@@ -694,8 +707,9 @@ def paged_copy(store: PagedStore, src: torch.Tensor, dst: torch.Tensor, stream=N
     dev = _one_device(stream, src, dst, store._buffers[0])
     if _current_device() != dev:
         return _on_device(dev, paged_copy, store, src, dst, stream)
-    check(h3kv_paged_copy(store._ref, src.data_ptr(), dst.data_ptr(), src.shape[0], _handle(dev, stream)),
-          "h3kv_paged_copy")
+    st = h3kv_paged_copy(store._ref, src.data_ptr(), dst.data_ptr(), src.shape[0], _handle(dev, stream))
+    if st != H3KV_OK:
+        _check_apart(st, "h3kv_paged_copy", store.tensors(), dict(src=src, dst=dst))
 
 
 def _need_table(page_table, lengths, cu_nodes) -> int:
@@ -730,9 +744,12 @@ def paged_keep(store: PagedStore, page_table: torch.Tensor, lengths: torch.Tenso
     else:
         _need_index(out, "out", (seqs,))
         _need_apart(out, lengths=lengths, cu_nodes=cu_nodes, page_table=page_table, keep=keep)
-    check(h3kv_paged_keep(store._ref, page_table.data_ptr(), page_table.shape[1], lengths.data_ptr(),
-                          cu_nodes.data_ptr(), seqs, keep.data_ptr(), keep.shape[0], out.data_ptr(),
-                          _handle(dev, stream)), "h3kv_paged_keep")
+    st = h3kv_paged_keep(store._ref, page_table.data_ptr(), page_table.shape[1], lengths.data_ptr(),
+                         cu_nodes.data_ptr(), seqs, keep.data_ptr(), keep.shape[0], out.data_ptr(),
+                         _handle(dev, stream))
+    if st != H3KV_OK:
+        _check_apart(st, "h3kv_paged_keep", dict(store.tensors(), out=out),
+                     dict(page_table=page_table, lengths=lengths, cu_nodes=cu_nodes, keep=keep))
     return out
 
 
@@ -770,10 +787,14 @@ def attend_tree(Q: torch.Tensor, store: PagedStore, page_table: torch.Tensor, le
     else:
         o = _need_strided(out, "out", heads, nodes)
         _need_apart(out, Q=Q, lse=lse, workspace=workspace)
-    check(h3kv_attend_tree(ctypes.byref(q), heads, nodes, store._ref, page_table.data_ptr(), page_table.shape[1],
-                           lengths.data_ptr(), cu_nodes.data_ptr(), seqs, 0 if parents is None else parents.data_ptr(),
-                           softmax_scale, ctypes.byref(o), 0 if lse is None else lse.data_ptr(),
-                           workspace.data_ptr(), workspace.numel(), _handle(dev, stream)), "h3kv_attend_tree")
+    st = h3kv_attend_tree(ctypes.byref(q), heads, nodes, store._ref, page_table.data_ptr(), page_table.shape[1],
+                          lengths.data_ptr(), cu_nodes.data_ptr(), seqs, 0 if parents is None else parents.data_ptr(),
+                          softmax_scale, ctypes.byref(o), 0 if lse is None else lse.data_ptr(),
+                          workspace.data_ptr(), workspace.numel(), _handle(dev, stream))
+    if st != H3KV_OK:
+        _check_apart(st, "h3kv_attend_tree", dict(out=out, lse=lse, workspace=workspace),
+                     dict(Q=Q, page_table=page_table, lengths=lengths, cu_nodes=cu_nodes, parents=parents,
+                          **store.tensors()))
     return out
 
 
@@ -809,10 +830,11 @@ def attend_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch
     else:
         o = _need_strided(out, "out", heads, rows)
         _need_apart(out, Q=Q, K=K, V=V, lse=lse)
-    check(h3kv_attend_prompt(ctypes.byref(q), heads, rows, ctypes.byref(k), ctypes.byref(v), kv_heads, k_rows,
-                             cu_q.data_ptr(), cu_k.data_ptr(), shape[0] - 1, bool(causal), softmax_scale,
-                             ctypes.byref(o), 0 if lse is None else lse.data_ptr(), _handle(dev, stream)),
-          "h3kv_attend_prompt")
+    st = h3kv_attend_prompt(ctypes.byref(q), heads, rows, ctypes.byref(k), ctypes.byref(v), kv_heads, k_rows,
+                            cu_q.data_ptr(), cu_k.data_ptr(), shape[0] - 1, bool(causal), softmax_scale,
+                            ctypes.byref(o), 0 if lse is None else lse.data_ptr(), _handle(dev, stream))
+    if st != H3KV_OK:
+        _check_apart(st, "h3kv_attend_prompt", dict(out=out, lse=lse), dict(Q=Q, K=K, V=V, cu_q=cu_q, cu_k=cu_k))
     return out
 
 

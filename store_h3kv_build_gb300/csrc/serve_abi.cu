@@ -3,8 +3,16 @@
 #include <math.h>
 
 #include "serve.h"
+#include "spans.h"
 
 namespace {
+
+using h3kv::meet;
+using h3kv::meets_any;
+using h3kv::meets_store;
+using h3kv::rows_meet;
+using h3kv::Span;
+using h3kv::span;
 
 // Rows are addressed with 32-bit numbers.
 constexpr int64_t kMaxRows = (1ll << 31) - 256;
@@ -88,6 +96,9 @@ h3kv_status h3kv_paged_append(const h3kv_rows *K, const h3kv_rows *V, const int3
   if (n < 0 || n > kMaxRows) return H3KV_ERR_INVALID_ARG;
   if (n == 0 || p.kv_heads == 0) return H3KV_OK;
   if (!rows_ok(K, p.kv_heads, n) || !rows_ok(V, p.kv_heads, n) || !rows || !aligned(rows, 4)) return H3KV_ERR_INVALID_ARG;
+  if (meets_store(span(*K, p.kv_heads, n), *store) || meets_store(span(*V, p.kv_heads, n), *store) ||
+      meets_store(span(rows, 4 * n), *store))
+    return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   p.err = d.err;
@@ -103,6 +114,9 @@ h3kv_status h3kv_paged_read(const h3kv_paged_store *store, const int32_t *rows, 
   if (n == 0 || p.kv_heads == 0) return H3KV_OK;
   if (!out_rows_ok(K, p.kv_heads, n) || !out_rows_ok(V, p.kv_heads, n) || !rows || !aligned(rows, 4))
     return H3KV_ERR_INVALID_ARG;
+  const Span k = span(*K, p.kv_heads, n), v = span(*V, p.kv_heads, n), r = span(rows, 4 * n);
+  if (rows_meet(*K, *V, p.kv_heads, n) || meet(k, r) || meet(v, r) || meets_store(k, *store) || meets_store(v, *store))
+    return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   p.err = d.err;
@@ -117,6 +131,7 @@ h3kv_status h3kv_paged_copy(const h3kv_paged_store *store, const int32_t *src, c
   if (n < 0 || n > kMaxRows / 16) return H3KV_ERR_INVALID_ARG;
   if (n == 0 || p.kv_heads == 0) return H3KV_OK;
   if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return H3KV_ERR_INVALID_ARG;
+  if (meets_store(span(src, 4 * n), *store) || meets_store(span(dst, 4 * n), *store)) return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   p.err = d.err;
@@ -134,8 +149,13 @@ h3kv_status h3kv_paged_keep(const h3kv_paged_store *store, const int32_t *page_t
   if (seqs == 0) return H3KV_OK;
   if (!lengths || !cu_nodes || !new_lengths || (!keep && nodes > 0)) return H3KV_ERR_INVALID_ARG;
   if (!aligned(lengths, 4) || !aligned(cu_nodes, 4) || !aligned(new_lengths, 4)) return H3KV_ERR_INVALID_ARG;
-  // lengths are read by every head's CTA while new_lengths is written
-  if (new_lengths < lengths + seqs && lengths < new_lengths + seqs) return H3KV_ERR_INVALID_ARG;
+  // the others are read by every head's CTA while new_lengths is written
+  const Span in[] = {span(lengths, 4ll * seqs), span(cu_nodes, 4ll * (seqs + 1)),
+                     span(page_table, 4 * seqs * max_pages), span(keep, nodes)};
+  if (meets_any(span(new_lengths, 4ll * seqs), in) || meets_store(span(new_lengths, 4ll * seqs), *store))
+    return H3KV_ERR_INVALID_ARG;
+  for (const Span &x : in)
+    if (meets_store(x, *store)) return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   p.err = d.err;
@@ -171,6 +191,17 @@ h3kv_status h3kv_attend_tree(const h3kv_rows *Q, int32_t q_heads, int64_t nodes,
   if (!workspace || !aligned(workspace, 32) ||
       workspace_bytes < h3kv::tree_workspace_bytes(q_heads, a.p.kv_heads, nodes, seqs))
     return H3KV_ERR_INVALID_ARG;
+  // what is written lies apart from the rest (O over Q is the caller's: a row of
+  // Q has been read before that of O is written)
+  const Span o = span(*O, q_heads, nodes), z = span(lse, 4 * q_heads * nodes),
+             ws = span(workspace, static_cast<int64_t>(h3kv::tree_workspace_bytes(q_heads, a.p.kv_heads, nodes, seqs)));
+  const Span in[] = {span(page_table, 4 * seqs * max_pages), span(lengths, 4ll * seqs), span(cu_nodes, 4ll * (seqs + 1)),
+                     span(parents, 4 * nodes)};
+  if (meet(o, z) || meet(o, ws) || meet(z, ws) || meet(z, span(*Q, q_heads, nodes)) ||
+      meet(ws, span(*Q, q_heads, nodes)))
+    return H3KV_ERR_INVALID_ARG;
+  for (const Span &x : {o, z, ws})
+    if (meets_any(x, in) || meets_store(x, *store)) return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;
   if ((st = h3kv::serve_device(&d)) != H3KV_OK) return st;
   a.p.err = d.err;
@@ -205,6 +236,13 @@ h3kv_status h3kv_attend_prompt(const h3kv_rows *Q, int32_t q_heads, int64_t q_ro
   if (!rows_ok(Q, q_heads, q_rows) || !out_rows_ok(O, q_heads, q_rows)) return H3KV_ERR_INVALID_ARG;
   if (k_rows > 0 && (!rows_ok(K, kv_heads, k_rows) || !rows_ok(V, kv_heads, k_rows))) return H3KV_ERR_INVALID_ARG;
   if (!cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(lse, 4)) return H3KV_ERR_INVALID_ARG;
+  // what is written lies apart from the rest (O over Q, and O beside Q, K and V
+  // in one buffer, is the caller's)
+  const Span o = span(*O, q_heads, q_rows), z = span(lse, 4 * q_heads * q_rows);
+  const Span cu[] = {span(cu_q, 4ll * (seqs + 1)), span(cu_k, 4ll * (seqs + 1))};
+  if (meet(o, z) || meets_any(o, cu) || meets_any(z, cu) || meet(z, span(*Q, q_heads, q_rows)) ||
+      (k_rows > 0 && (meet(z, span(*K, kv_heads, k_rows)) || meet(z, span(*V, kv_heads, k_rows)))))
+    return H3KV_ERR_INVALID_ARG;
   h3kv::ServeDevice d;
   const h3kv_status st = h3kv::serve_device(&d);
   if (st != H3KV_OK) return st;
