@@ -340,7 +340,7 @@ h3kv_status h3kv_sync_status(void *stream);
  * records H3KV_ERR_DEVICE_TIMEOUT, drains its own copies and MMAs, and exits
  * with its output undefined, leaving the context usable.  A wait for the end
  * of a run of key tiles (h3kv_attend_prompt, h3kv_attend_tree) has this limit
- * for each of them.  A wait whose
+ * for each key tile that the call's sequences may have.  A wait whose
  * phase completes while its first (suspended) poll is pending never runs
  * out, however small the limit (see h3kv_debug_withhold_p). */
 h3kv_status h3kv_set_wait_timeout_ns(uint64_t timeout_ns);

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const WaitCtx w{a.err, &sm.abort, a.timeout_ns};
+  const WaitCtx long_wait{a.err, &sm.abort, a.segment_timeout_ns};  // for the end of a segment
   SegReader<PromptSegs> sr;
 
   if (warp < 8) {
@@ -264,19 +265,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dealloc<kRegZero>();
     Ring<kNV> vr;
     uint32_t phase = 0;
-    int n = 0;
     bool ok = true;
-    while (ok && (ok = sr.get(sm.segs, for_tiles(w, n)))) {
+    while (ok && (ok = sr.get(sm.segs, long_wait))) {
       const Seg &s = sr.seg(sm.segs);
-      const int rows = s.rows;
-      n = s.n;
+      const int n = s.n, rows = s.rows;
       const bool ragged = is_ragged(s);
       const int valid = static_cast<int>(s.keys - static_cast<int64_t>(n - 1) * kBN);
       sr.done(sm.segs);
       if (rows == 0) break;
       for (int t = 0; t < n; ++t) {
         if (ragged && t == n - 1) {
-          if (!(ok = warp_wait(smem_u32(&sm.v_tail), phase, for_tiles(w, n)))) break;
+          if (!(ok = warp_wait(smem_u32(&sm.v_tail), phase, long_wait))) break;
           phase ^= 1u;
           const int r = (warp - 8) * 32 + lane;
           if (r >= valid) {
@@ -378,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<PromptSegs::kDepth> r;
       uint32_t block = blockIdx.x, phase = 0, copies_phase = 0;
       bool more = true;
-      int before = 0;  // key tiles of the segment before
       auto next_block = [&] {
         if (lane == 0) request_block(smem_u32(sm.taken), smem_u32(&sm.taken_bar));
         const bool came = warp_wait(smem_u32(&sm.taken_bar), phase, w);
@@ -398,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           more = next_block();  // (a block that no sequence needs)
         }
         if (!found) s.rows = s.n = 0;
-        if (!warp_wait(smem_u32(&sm.segs.empty[r.slot]), r.phase ^ 1u, for_tiles(w, before))) break;
+        if (!warp_wait(smem_u32(&sm.segs.empty[r.slot]), r.phase ^ 1u, long_wait)) break;
         if (lane == 0) {
           sm.segs.seg[r.slot] = s;
           mbar_arrive(smem_u32(&sm.segs.full[r.slot]));
@@ -409,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // another block is asked for only when this segment's last copies are
         // under way (two tiles before its end): taken earlier, it would wait
         // here while other SMs run out of work
-        before = s.n;
-        if (!warp_wait(smem_u32(&sm.last_copies), copies_phase, for_tiles(w, s.n))) break;
+        if (!warp_wait(smem_u32(&sm.last_copies), copies_phase, long_wait)) break;
         copies_phase ^= 1u;
         more = next_block();
       }

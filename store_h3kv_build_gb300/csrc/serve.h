@@ -73,7 +73,7 @@ struct TreeArgs {
   int32_t ctas;
   int32_t item_rows;   // rows of a row tile, by the kernel that runs, and
   int32_t item_cost;   //   what one costs beside its key tiles, in tiles
-  uint64_t timeout_ns;
+  uint64_t timeout_ns, segment_timeout_ns;  // of a wait, and of one for a segment's end
   int32_t withhold_p_tile1;
 };
 size_t tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64_t nodes, int32_t seqs);
@@ -91,7 +91,7 @@ struct PromptArgs {
   int32_t q_heads, kv_heads, group, seqs, causal;
   float scale_log2;
   uint32_t *err;
-  uint64_t timeout_ns;
+  uint64_t timeout_ns, segment_timeout_ns;
   int32_t withhold_p_tile1;
   int32_t num_sms;
 };

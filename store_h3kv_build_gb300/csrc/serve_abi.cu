@@ -71,6 +71,14 @@ float scale_log2_of(float softmax_scale) {
   return s * 1.4426950408889634f;
 }
 
+// The limit of a wait for the end of a segment of up to `keys` keys: that of a
+// wait for each key tile (where a tile hangs, its own wait runs out first and
+// ends this one).
+uint64_t segment_timeout(uint64_t timeout_ns, int64_t keys) {
+  const uint64_t n = static_cast<uint64_t>(keys) / H3KV_KV_TILE + 8;
+  return timeout_ns > UINT64_MAX / n ? UINT64_MAX : timeout_ns * n;
+}
+
 // Page tables are addressed as [seqs, max_pages] of 4-byte entries.
 bool table_ok(const int32_t *page_table, int64_t max_pages) {
   return max_pages >= 0 && max_pages <= kMaxRows / 16 && aligned(page_table, 4) && (page_table || max_pages == 0);
@@ -221,6 +229,7 @@ h3kv_status h3kv_attend_tree(const h3kv_rows *Q, int32_t q_heads, int64_t nodes,
   a.workspace = static_cast<float *>(workspace);
   a.ctas = d.num_sms;
   a.timeout_ns = d.timeout_ns;
+  a.segment_timeout_ns = segment_timeout(d.timeout_ns, max_pages * a.p.page_size);
   a.withhold_p_tile1 = d.withhold_p_tile1;
   return status_of(h3kv::launch_attend_tree(a, static_cast<cudaStream_t>(stream)));
 }
@@ -266,6 +275,7 @@ h3kv_status h3kv_attend_prompt(const h3kv_rows *Q, int32_t q_heads, int64_t q_ro
   a.scale_log2 = scale_log2_of(softmax_scale);
   a.err = d.err;
   a.timeout_ns = d.timeout_ns;
+  a.segment_timeout_ns = segment_timeout(d.timeout_ns, k_rows);
   a.withhold_p_tile1 = d.withhold_p_tile1;
   a.num_sms = d.num_sms;
   return status_of(h3kv::launch_attend_prompt(a, static_cast<cudaStream_t>(stream)));

@@ -117,14 +117,6 @@ __device__ __forceinline__ int tile_step(const Seg &s) { return s.two ? 1 : 2; }
 __device__ __forceinline__ int end_tile(const Seg &s, int q) { return s.two && q == 0 ? s.n0 : s.n; }
 __device__ __forceinline__ bool has_tiles(const Seg &s, int q) { return first_tile(s, q) < end_tile(s, q); }
 
-// The limit of a wait for what comes at the end of `tiles` key tiles: the limit
-// of a wait for each of them (where a tile hangs, its own wait runs out first
-// and ends this one).
-__device__ __forceinline__ WaitCtx for_tiles(const WaitCtx &w, int tiles) {
-  const uint64_t n = static_cast<uint64_t>(tiles) + 8;
-  return {w.err, w.abort, __umul64hi(w.timeout_ns, n) ? ~0ull : w.timeout_ns * n};
-}
-
 // The segments go through a short ring in shared memory: one warp finds
 // them (its 64-bit divisions and counts would otherwise take registers and
 // instruction cache in every role), the others read.  A segment of no tiles is the end.

@@ -268,13 +268,11 @@ __device__ __forceinline__ void publish_segments(const TreeArgs &a, const Scan &
   walk.start(a, sc);
   Ring<TreeSegs::kDepth> r;
   bool described = false;
-  int last = 0, before = 0;  // key tiles of the last segment and the one before
+  const WaitCtx long_wait{w.err, w.abort, a.segment_timeout_ns};  // a slot falls free when its segment is done
   for (;;) {
     Seg s;
     const bool more = walk.next(a, &s);
-    if (!warp_wait(smem_u32(&ring.empty[r.slot]), r.phase ^ 1u, for_tiles(w, last + before))) return;
-    before = last;
-    last = s.n;
+    if (!warp_wait(smem_u32(&ring.empty[r.slot]), r.phase ^ 1u, long_wait)) return;
     if ((threadIdx.x & 31) == 0) {
       ring.seg[r.slot] = s;
       mbar_arrive(smem_u32(&ring.full[r.slot]));
