@@ -105,7 +105,6 @@ struct Finder {
       k0 = __shfl_sync(0xffffffffu, k0, src);
       k1 = __shfl_sync(0xffffffffu, k1, src);
       Seg s;
-      s.seq = base + src;
       s.head = static_cast<int>(block - static_cast<uint32_t>(unit) * a.q_heads);
       s.row0 = static_cast<int>(tile * tile_rows);
       const int64_t left = q1 - q0 - s.row0;

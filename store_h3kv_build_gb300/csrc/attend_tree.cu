@@ -7,8 +7,9 @@
 // share: 1.9 us for 256 rows over a 128-key tile, where the products alone take
 // 1.3 (the tensor rate) and the bytes 0.75.  A segment costs some 12 us more
 // before its first tile (counts, query rows, first page) and 4 behind its last.
-// Measured at 64 nodes, 32 query heads over 8: 2 x 131072 cached rows 228 us
-// (1180 TFLOP/s), 32 x 8192 250 us, 128 x 2048 329 us, 512 x 512 507 us.
+// A thread spills 56 bytes.  Measured at 64 nodes, 32 query heads over 8: 2 x
+// 131072 cached rows 228 us (1207 TFLOP/s), 32 x 8192 250 us, 128 x 2048 334 us,
+// 512 x 512 506 us.
 #include "store_fwht.cuh"
 #include "tree.cuh"
 

@@ -11,15 +11,20 @@
 //   rows <= 128:         both own the same rows, warpgroup q sees the key tiles
 //                        of parity q, and the two running softmaxes are joined
 //                        by their log-sum-exp at the segment's end.
-// So a single token keeps both halves of the pipeline busy, and its keys are
-// read once.
+// So few rows keep both halves of the pipeline busy too, and their keys are
+// read once.  (Trees of up to 32 rows a sequence and kv head have a kernel of
+// their own.)
 //
 // Warp roles (512 threads):
 //   warps 0-3, 4-7  softmax, correction and epilogue of stream 0 / 1
 //   warps 8-11      cache: in-place int8 -> fp16 dequantisation of K and V
-//                   tiles; prompts: zeroing of the V rows behind a sequence
-//   warp 12         producer: bulk / TMA copies into the K and V rings
+//                   tiles, query rows of later segments; prompts: zeroing of
+//                   the V rows behind a sequence
+//   warp 12         prompts: TMA copies of Q, K and V; cache: bulk copies of
+//                   K's codes
 //   warp 13         TMEM allocation and tcgen05.mma issue
+//   warp 14         cache: bulk copies of V's codes; prompts: idle
+//   warp 15         finds the segments
 // TMEM (512 columns, fp32): S0 [0,128), S1 [128,256), P over the first 64
 // columns of its S, O0 [256,384), O1 [384,512).
 #pragma once
@@ -107,7 +112,9 @@ struct Seg {
   int64_t k_base; // prompt: first row of the sequence in K; cache: its first page table entry
   int64_t diff;   // prompt, causal: row t sees the keys u <= t + diff
   int nodes;      // cache: drafted nodes
-  int seq;
+  int seq;        // cache: not read; without it ptxas allots the few-row kernel's
+                  // registers otherwise, and items of 32 rows (8 nodes of four
+                  // heads over 32 x 8192 rows) took 169 us in place of 161
   int whole;      // every key tile of the rows is in this segment
 };
 

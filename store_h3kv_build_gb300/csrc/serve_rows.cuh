@@ -20,12 +20,6 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// The same in groups: all but the last kPending of this thread's are done.
-__device__ __forceinline__ void copy16_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void copy16_wait_but() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
 
 // TMA store of a box from shared memory, in groups of this thread's own; at
 // most kPending groups may still be reading shared memory after the wait.
