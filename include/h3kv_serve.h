@@ -5,6 +5,9 @@
  * dropped -- with the attention of a tree of drafted tokens (a single new
  * token is the tree of one node) over it.
  *
+ * ABI version 9 libraries exist without these entry points: a caller that loads
+ * the library looks them up by name.
+ *
  * The conventions of h3kv.h hold here too: host-side checks before any
  * launch, stream-ordered asynchronous calls, memory owned by the caller,
  * bounded waits.  What differs:
@@ -13,7 +16,8 @@
  *  - Index arrays (row and page numbers, lengths, cumulative counts, parents)
  *    are int32 in device memory, so that a captured graph takes new ones at
  *    each replay.  The host cannot check them: a kernel that meets an entry
- *    out of range leaves that entry's work out, touches no memory for it, and
+ *    out of range leaves that entry's work out, touches no memory that it
+ *    names (h3kv_attend_tree reads page 0 in the place of such a page), and
  *    h3kv_sync_status() then returns H3KV_ERR_DEVICE_DATA.  The output of the
  *    sequence concerned is undefined.
  *  - Packed tensors: the rows cu[i] .. cu[i+1]-1 belong to sequence i.  Rows
@@ -116,7 +120,10 @@ size_t h3kv_attend_tree_workspace_bytes(int32_t q_heads, int32_t kv_heads, int64
  * A cached row that is not finite (a scale of NaN, or code * scale beyond fp16)
  * may reach every node of its own sequence, also those that do not see it, and
  * none of another's.
- * q_heads / kv_heads is at most 64.  The keys of a sequence are split over
+ * q_heads / kv_heads is at most 64.  The kernel is chosen by the mean count of
+ * rows, q_heads nodes / (kv_heads seqs), since the host does not know the single
+ * counts: sequences without nodes among seqs make one with many slow, not
+ * wrong.  The keys of a sequence are split over
  * the GPU's SMs and joined by their log-sum-exp in a fixed order: the same
  * call gives the same bits, another batch around a sequence may round
  * differently. */
