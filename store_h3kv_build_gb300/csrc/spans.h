@@ -24,7 +24,9 @@ inline __int128 extent(const h3kv_rows &r, int64_t heads, int64_t rows) {
          (rows > 1 ? static_cast<__int128>(rows - 1) * r.row_stride : 0) + H3KV_HEAD_DIM;
 }
 inline Span span(const h3kv_rows &r, int64_t heads, int64_t rows) { return span(r.data, 2 * extent(r, heads, rows)); }
-inline bool meet(const Span &a, const Span &b) { return a.begin < b.end && b.begin < a.end; }
+inline bool meet(const Span &a, const Span &b) {
+  return a.begin < b.end && b.begin < a.end && a.begin < a.end && b.begin < b.end;
+}
 template <int kN>
 inline bool meets_any(const Span &a, const Span (&others)[kN]) {
   for (const Span &o : others)

@@ -40,6 +40,7 @@ int main() {
   if (span(far, 65535, (1ll << 31) - 256).end != UINTPTR_MAX) ++wrong;
   if (span(far, 2, 1).end != reinterpret_cast<uintptr_t>(base) + 2 * ((1ull << 38) - 8 + 128)) ++wrong;
   if (meet(span(nullptr, 64), span(nullptr, 64))) ++wrong;  // an absent tensor
+  if (meet(span(base + 8, 0), span(base, 64)) || meet(span(base, 64), span(base + 8, 0))) ++wrong;  // an empty one
   printf("cases %ld, meeting %ld, apart within each other's extent %ld, wrong %ld\n", cases, met, apart_within, wrong);
   return wrong != 0;
 }
