@@ -109,7 +109,7 @@ size_t h3kv_attend_paged_f8_workspace_bytes(int32_t q_heads, int32_t kv_heads, i
  *   S = Q K'^T softmax_scale, O = bf16(softmax(S) V'), K' and V' the cached
  *   values; a query element is exact (fp16 for few rows; for many the sum of two
  *   e4m3 parts, exact down to 2^-10 of the row's largest element and within
- *   2^-17 of that below); weights rounded to fp16 for the second product (down to
+ *   2^-17 of that below, or within 2^-76); weights rounded to fp16 for the second product (down to
  *   2^-32 of the largest), fp32 sums;  softmax_scale and lse as h3kv_attend_tree.
  * A row of Q with an element beyond 65504, an infinity or NaN gives an undefined
  * row of O.  A cached row that is not finite may reach every row of its own

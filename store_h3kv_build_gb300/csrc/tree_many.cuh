@@ -101,7 +101,11 @@ __device__ __forceinline__ void produce(const TreeArgs &a, S &sm, uint8_t (&ring
 // e4m3: the producer warp of K.  Whole pages by TMA with the 128-byte swizzle
 // (what lies behind the sequence is masked in the scores), and for each run of 16
 // keys what its scores are multiplied with: fp16(scale) times softmax_scale in log2
-// units; behind the sequence 1.  (Positive, so that masked scores stay -infinity.)
+// units; behind the sequence 1.  At least 2^-60: times a query row's factor, at least
+// 2^-66 (split_row), it is no less than fp32's least normal number, so that a masked
+// score stays -infinity and is never -infinity times 0.  A factor below that belongs
+// to scores that do not count: 128 products of a code (at most 448) and a query
+// element (at most 65504, 2^16) come to less than 2^32, times 2^-60 to 2^-28 in log2 units.
 __device__ __forceinline__ void produce_keys(const TreeArgs &a, TreeSmem<true> &sm, const CUtensorMap *map,
                                              const WaitCtx &w) {
   constexpr int kDepth = SmemT<true>::kKeyTiles;
@@ -143,7 +147,7 @@ __device__ __forceinline__ void produce_keys(const TreeArgs &a, TreeSmem<true> &
       if (at < valid) tma_load_2d(smem_u32(sm.k[r.slot]) + at * 128, map, 0, row, bar);
       if (at16 < kBN) {
         float f = __half2float(__float2half_rn(scale)) * a.scale_log2;
-        asm("max.NaN.f32 %0, %0, 0f0DA24260;" : "+f"(f));  // at least 1e-30; NaN stays
+        asm("max.NaN.f32 %0, %0, 0f21800000;" : "+f"(f));  // at least 2^-60; NaN stays
         sm.ks[tile % kScaleTiles][lane] = at16 < valid ? f : 1.f;
         mbar_arrive(bar);
       }
@@ -160,16 +164,18 @@ __device__ __forceinline__ void produce_keys(const TreeArgs &a, TreeSmem<true> &
 // e4m3: a row's lane (values 8l .. 8l+7 and 64 + 8l ..) as the sum of two e4m3 parts
 // times a power of two that all its lanes share: the first part leaves at most 4
 // bits of a bf16 value's 8, which the second holds exactly, but for values below
-// 2^-10 of the row's largest, where it rounds to 2^-17 of that.
+// 2^-10 of the row's largest, where it rounds to 2^-17 of that.  The power is 2^-66 or
+// more (see produce_keys), so a row whose largest element is below 224 2^-66 holds its
+// elements to 2^-76.
 __device__ __forceinline__ float split_row(const float (&v)[16], uint2 (&hi)[2], uint2 (&lo)[2]) {
   float top = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
   for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  // least e with top <= 448 2^e, kept where 2^e and 2^-e are fp32 numbers
+  // least e with top <= 448 2^e, at least -66, and kept where 2^-e is an fp32 number
   const uint32_t u = __float_as_uint(top);
-  const int e = min(max(static_cast<int>(u >> 23) - 135 + ((u & 0x7FFFFFu) > 0x600000u), -100), 120);
+  const int e = min(max(static_cast<int>(u >> 23) - 135 + ((u & 0x7FFFFFu) > 0x600000u), -66), 120);
   const float m = __int_as_float((127 - e) << 23);
   uint32_t c[2][4];
 #pragma unroll

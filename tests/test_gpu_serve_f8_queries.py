@@ -1,0 +1,39 @@
+"""Query rows of any size through the attention over e4m3 pages, on the kernel for
+few rows (items of 8, 16 and 32) and on both softmaxes of the one for many."""
+import pytest
+import torch
+
+from oracle import serve_f8 as so
+from store_h3kv_build_gb300 import binding as b
+
+from test_gpu_serve_f8 import DEV, arrays_of, cu_of, filled, i32, normal, within
+
+pytestmark = pytest.mark.gpu
+
+ROWS = [1, 3, 7, 20, 300]  # tokens of 4 heads: 4, 12, 28, 80 and 1200 rows
+
+
+def check(q, st, table, lens, news, scale, what):
+    cu = cu_of(news)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    o = b.attend_paged_f8(q.to(DEV), st, torch.from_numpy(table).to(DEV), i32(lens), i32(cu), scale, lse=lse)
+    b.sync_status()
+    ref = so.attend(q, arrays_of(st), table, lens, cu, scale if scale > 0 else None)
+    within(o, ref[0], ref[2], what)
+    within(lse, ref[1], ref[3], what + " lse")
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("ps", [16, 64])
+@pytest.mark.parametrize("k_scale,scale", [(2.0 ** -30, 0.0), (None, 1e-18), (2.0 ** -30, 1e-12), (2.0 ** -20, 1e-30)])
+def test_rows_of_zeros_and_factors_next_to_zero(cuda, m, ps, k_scale, scale):
+    # every score is next to nothing, so that a row is the mean of the V that it sees
+    lens = [m + 130, m + 1]
+    st, table = filled(lens, 1, ps, m, bad=False)
+    if k_scale is not None:
+        st.k_scales.fill_(k_scale)
+    q = normal(m, 4, 2 * m, 128)
+    q[:, ::3] = 0
+    q[1] *= 2.0 ** -100
+    q[2] = 0
+    check(q, st, table, lens, [m, m], scale, f"{m} {ps}")
