@@ -107,12 +107,15 @@ size_t h3kv_attend_paged_f8_workspace_bytes(int32_t q_heads, int32_t kv_heads, i
  * tokens of sequence i (appended before), one or many of them, and the last
  * row sees every token, each row before it one less.
  *   S = Q K'^T softmax_scale, O = bf16(softmax(S) V'), K' and V' the cached
- *   values; a query element is exact (fp16 for few rows; for many the sum of two
- *   e4m3 parts, exact down to 2^-10 of the row's largest element and within
- *   2^-17 of that below, or within 2^-76); weights rounded to fp16 for the second product (down to
- *   2^-32 of the largest), fp32 sums;  softmax_scale and lse as h3kv_attend_tree.
- * A row of Q with an element beyond 65504, an infinity or NaN gives an undefined
- * row of O.  A cached row that is not finite may reach every row of its own
+ *   values; weights rounded to fp16 for the second product (down to 2^-32 of the
+ *   largest), fp32 sums;  softmax_scale and lse as h3kv_attend_tree.
+ * A query row is taken times a power of two.  For few rows as fp16, exact for
+ * elements down to 2^-31 of the row's largest and within 2^-39 of that below; for
+ * many as the sum of two e4m3 parts, exact down to 2^-9 of the largest and within
+ * 2^-17 of that below, or within 2^-76 (a row with channels far above the rest keeps
+ * fewer bits of these).  A row of Q with an element beyond 65504, an infinity or NaN
+ * gives an undefined row of O.
+ * A cached row that is not finite may reach every row of its own
  * sequence, and none of another's.  Splitting of the keys, determinism and the
  * workspace are those of h3kv_attend_tree.  The kernel is chosen by the mean
  * count of rows, q_heads n / (kv_heads seqs) -- up to 16 for few, from 33 on for

@@ -3,7 +3,7 @@ append, its values and the causal attention over it (test infrastructure only).
 
 Attention bounds are those of ``serve._softmax`` (fp16 weights, fp32 sums); the
 output is rounded to bf16 once.  K' and V' are exact for scales that the append
-writes, and Q is fp16(Q).
+writes.
 """
 from __future__ import annotations
 
@@ -83,10 +83,18 @@ def gather(codes, scales, table, length):
     return np.swapaxes(fp16_round(x), 0, 1)
 
 
-def attend(Q, arrays, table, lengths, cu, scale=None):
-    """-> (O, lse, bound of O, bound of lse); rows of no sequence are NaN."""
+def attend(Q, arrays, table, lengths, cu, scale=None, split=False):
+    """-> (O, lse, bound of O, bound of lse); rows of no sequence are NaN.
+
+    split: bounds for a query row as the sum of two e4m3 parts, scaled so that its
+    largest element lies in (224, 448].  A bf16 element of at least 2^-2 there has
+    a last bit of 2^-9 or more, which the second part's least step reaches: exact,
+    and so is one down to 2^-9 of the largest.  One below is off by at most half
+    that step, 2^-10 / 224 < 2^-17 of the largest."""
     Q = as_f64(Q)
-    q16 = fp16_round(Q)
+    size = np.abs(Q)
+    top = size.max(axis=-1, keepdims=True, initial=0.0)
+    lost = np.where((size > 0) & (size < top * 2.0 ** -9), 2.0 ** -17 * top, 0.0) if split else np.zeros(Q.shape)
     scale = default_scale() if scale is None else scale
     hk = arrays["k_codes"].shape[1]
     g = Q.shape[0] // hk
@@ -101,7 +109,8 @@ def attend(Q, arrays, table, lengths, cu, scale=None):
         v = gather(arrays["v_codes"], arrays["v_scales"], table[i], n)
         see = np.arange(n)[None, :] <= np.arange(n - m, n)[:, None]
         for h in range(Q.shape[0]):
-            o, z, off, zoff = _softmax(q16[h, c0:c1], k[h // g], v[h // g], see, scale, 0.0, U_FP16, 2.0 ** -25)
+            e = scale * (lost[h, c0:c1] @ np.abs(k[h // g]).T).max(axis=1)
+            o, z, off, zoff = _softmax(Q[h, c0:c1], k[h // g], v[h // g], see, scale, e, U_FP16, 2.0 ** -25)
             O[h, c0:c1], lse[h, c0:c1], bl[h, c0:c1] = o, z, zoff
             bo[h, c0:c1] = off + U_BF16 * np.abs(o) * (1 + 2.0 ** -7) + 2.0 ** -134
     return O, lse, bo, bl

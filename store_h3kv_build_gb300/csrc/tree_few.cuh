@@ -25,11 +25,12 @@
 // products and of what feeds them bounds it.
 //
 // e4m3: a code is an fp16 number, converted two at a time; a warp's 16 keys lie in
-// one page, so that K's scale multiplies the scores instead of the codes.  32 query
-// heads over 8, one token each: 32 x 8192 cached rows 93 us (5.8 TB/s; 7.5 between
-// the first tile, 5 us after the launch, and the join), 4 x 131072 74 us, 1 x 32768 19
-// us, 128 x 1024 55 us, 1 x 1024 8 and 5 us for the join; four tokens each of 32 x 8192
-// 105 us, of 128 x 1024 76 us, eight 117.
+// one page, so that K's scale multiplies the scores instead of the codes, and with it
+// the power of two that a query row was taken times (1.7 % for items of 16 rows).  32
+// query heads over 8, one token each: 32 x 8192 cached rows 92 us (5.8 TB/s; 7.5
+// between the first tile, 5 us after the launch, and the join), 4 x 131072 74 us, 1 x
+// 32768 19 us, 128 x 1024 54 us, 1 x 1024 8 and 5 us for the join; four tokens each of
+// 32 x 8192 106 us, of 128 x 1024 76 us, eight 122.
 #pragma once
 
 #include "tree.cuh"
@@ -60,6 +61,7 @@ struct FewSmem {
     float page_scale[kStages][2][kBN / 16];  // e4m3: of K's and V's runs of 16 keys
   };
   uint16_t q[TreeSegs::kDepth][8 * kNT][kQPitch];  // q' of a segment's rows, by its slot
+  float factor[kF8 ? TreeSegs::kDepth : 1][kF8 ? 8 * kNT : 1];  // e4m3: of their scores
   float m[kWarps][8 * kNT], l[kWarps][8 * kNT];
   uint64_t path[TreeSegs::kDepth][8 * kNT];  // e4m3: the keys that the row sees
   uint64_t full[kStages], empty[kStages], q_full[TreeSegs::kDepth];
@@ -92,15 +94,31 @@ __device__ __forceinline__ uint32_t scale2(uint32_t x, uint32_t s) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// q' = fp16(q H), e4m3: fp16(q), of a row in place, by 8 lanes (l: the lane among
-// them).
+// q' = fp16(q H) of a row in place, by 8 lanes (l: the lane among them).  e4m3: q' = q
+// 2^-e, with the row's largest element in [2^14, 2^15): fp16 holds a bf16 element whose
+// last bit is 2^-24 or more there, exactly (down to 2^-31 of the largest), and any
+// other to half of that, 2^-39 of the largest.  c2 2^e, which the row's scores are
+// multiplied with beside K's scale, goes to `factor`.  (fp16(q) loses what lies below
+// 2^-17, whatever the row's size.)
 template <bool kF8>
-__device__ __forceinline__ void rotate_row(uint16_t (&row)[kQPitch], int l) {
+__device__ __forceinline__ void rotate_row(uint16_t (&row)[kQPitch], int l, float c2, float *factor) {
   uint4 *dst = reinterpret_cast<uint4 *>(row) + l;
   float v[16];
   unpack_bf16x8(dst[0], v);
   unpack_bf16x8(dst[8], v + 8);
-  if constexpr (!kF8) {
+  if constexpr (kF8) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    // (kept where 2^-e is an fp32 number)
+    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 141, -100);
+    const float m = __int_as_float((127 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] *= m;
+    if (l == 0) *factor = c2 * __int_as_float((127 + e) << 23);
+  } else {
     fwht128_oct(v, l);
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] *= kInvSqrt128;
@@ -177,7 +195,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         copy16_wait();
         if constexpr (kAhead) {
 #pragma unroll 1
-          for (int row = lane >> 3; row < 8 * kNT; row += 4) rotate_row<kF8>(sm.q[slot][row], l);
+          for (int row = lane >> 3; row < 8 * kNT; row += 4)
+            rotate_row<kF8>(sm.q[slot][row], l, a.scale_log2, kF8 ? &sm.factor[slot][row] : nullptr);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
@@ -271,7 +290,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const Seg &s = sr.seg(sm.segs);
     const int qs = sr.r.slot;
     if (ok && s.n > 0) ok = warp_wait(smem_u32(&sm.q_full[qs]), sr.r.phase, w);
-    if (!kAhead && ok && s.n > 0 && warp < 2 * kNT) rotate_row<kF8>(sm.q[qs][warp * 4 + (lane >> 3)], lane & 7);
+    if (!kAhead && ok && s.n > 0 && warp < 2 * kNT) rotate_row<kF8>(sm.q[qs][warp * 4 + (lane >> 3)], lane & 7, 0.f, nullptr);
     // the warps go on, or leave, together
     ok = named_bar_and(1, kWarps * 32, ok);
     if (!ok || s.n == 0) break;
@@ -313,7 +332,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // the step's codes and scales into registers, and the stage is free again
       uint4 kw[2][2], vw[4];
       uint32_t k0, k1, v0, v1;
-      float ck = c2;  // e4m3: times K's scale
+      // what the scores of rows 8 nt + 2 i4 + {0, 1} are multiplied with (read behind the
+      // products, e4m3 items of 16 rows took 2 % longer; kept for all tiles, too)
+      float2 ck[kNT];
       auto load_v = [&] {
         const uint8_t *vb = sm.v[r.slot] + v_row;
 #pragma unroll
@@ -341,10 +362,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           kw[hf][1] = *reinterpret_cast<const uint4 *>(kb + 8 * 128 + c);
         }
         if constexpr (kF8) {
-          ck *= __half2float(__float2half_rn(sm.page_scale[r.slot][0][warp]));
+          const float f = __half2float(__float2half_rn(sm.page_scale[r.slot][0][warp]));
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const float2 z = *reinterpret_cast<const float2 *>(&sm.factor[qs][8 * nt + 2 * i4]);
+            ck[nt] = make_float2(f * z.x, f * z.y);
+          }
         } else {
           k0 = sm.ks[r.slot][key0 + g8] * 0x10001u;
           k1 = sm.ks[r.slot][key0 + g8 + 8] * 0x10001u;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) ck[nt] = make_float2(c2, c2);
         }
       }
       if (!kBig || pos >= keys) load_v();
@@ -420,7 +448,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st[nt][e] = (st[nt][e] + su[nt][e]) * ck;
+          for (int e = 0; e < 4; ++e) st[nt][e] = (st[nt][e] + su[nt][e]) * (e & 1 ? ck[nt].y : ck[nt].x);
         }
         if (pos + 16 > base_key) {
           const int32_t n0 = pos + g8 - base_key, n1 = n0 + 8;

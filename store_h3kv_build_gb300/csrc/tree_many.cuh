@@ -162,9 +162,10 @@ __device__ __forceinline__ void produce_keys(const TreeArgs &a, TreeSmem<true> &
 }
 
 // e4m3: a row's lane (values 8l .. 8l+7 and 64 + 8l ..) as the sum of two e4m3 parts
-// times a power of two that all its lanes share: the first part leaves at most 4
-// bits of a bf16 value's 8, which the second holds exactly, but for values below
-// 2^-10 of the row's largest, where it rounds to 2^-17 of that.  The power is 2^-66 or
+// times a power of two that all its lanes share, with which the row's largest lies in
+// (224, 448]: the first part leaves at most 4 bits of a bf16 value's 8, which the second
+// holds exactly where they reach down to its least step, 2^-9: for values from 2^-2 on,
+// 2^-9 of the largest or less.  Below, it is off by half that step, 2^-17 of the largest.  The power is 2^-66 or
 // more (see produce_keys), so a row whose largest element is below 224 2^-66 holds its
 // elements to 2^-76.
 __device__ __forceinline__ float split_row(const float (&v)[16], uint2 (&hi)[2], uint2 (&lo)[2]) {

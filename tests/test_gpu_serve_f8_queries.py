@@ -1,8 +1,12 @@
-"""Query rows of any size through the attention over e4m3 pages, on the kernel for
-few rows (items of 8, 16 and 32) and on both softmaxes of the one for many."""
+"""Query rows of any size through the attention over e4m3 pages: zeros, rows far
+below and far above one, rows with channels far larger than the rest; on the
+kernel for few rows (items of 8, 16 and 32) and on both softmaxes of the one for
+many."""
+import numpy as np
 import pytest
 import torch
 
+import oracle
 from oracle import serve_f8 as so
 from store_h3kv_build_gb300 import binding as b
 
@@ -11,14 +15,15 @@ from test_gpu_serve_f8 import DEV, arrays_of, cu_of, filled, i32, normal, within
 pytestmark = pytest.mark.gpu
 
 ROWS = [1, 3, 7, 20, 300]  # tokens of 4 heads: 4, 12, 28, 80 and 1200 rows
+MANY = 20                  # from here on a query row is the sum of two e4m3 parts
 
 
-def check(q, st, table, lens, news, scale, what):
+def check(q, st, table, lens, news, scale, what, split=False):
     cu = cu_of(news)
     lse = torch.full(q.shape[:2], 7.0, device=DEV)
     o = b.attend_paged_f8(q.to(DEV), st, torch.from_numpy(table).to(DEV), i32(lens), i32(cu), scale, lse=lse)
     b.sync_status()
-    ref = so.attend(q, arrays_of(st), table, lens, cu, scale if scale > 0 else None)
+    ref = so.attend(q, arrays_of(st), table, lens, cu, scale if scale > 0 else None, split=split)
     within(o, ref[0], ref[2], what)
     within(lse, ref[1], ref[3], what + " lse")
 
@@ -37,3 +42,36 @@ def test_rows_of_zeros_and_factors_next_to_zero(cuda, m, ps, k_scale, scale):
     q[1] *= 2.0 ** -100
     q[2] = 0
     check(q, st, table, lens, [m, m], scale, f"{m} {ps}")
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("size", [-50, -40, -20, 12])
+def test_rows_of_any_size(cuda, m, size):
+    lens = [m + 200, m]
+    st, table = filled(lens, 2, 32, m, bad=False)
+    q = normal(m + 1, 8, 2 * m, 128) * 2.0 ** size
+    check(q, st, table, lens, [m, m], oracle.default_scale() * 2.0 ** -size, f"{m} {size}", split=m >= MANY)
+
+
+@pytest.mark.parametrize("m", ROWS)
+def test_rows_of_unlike_sizes(cuda, m):
+    # each row has its own power of two
+    lens = [m + 200, m]
+    st, table = filled(lens, 2, 32, m, bad=False)
+    q = normal(m + 1, 8, 2 * m, 128)
+    rng = np.random.default_rng(m)
+    q *= torch.from_numpy(2.0 ** -rng.integers(0, 40, (8, 2 * m, 1))).to(torch.bfloat16)
+    check(q, st, table, lens, [m, m], 3.0, f"{m}", split=m >= MANY)
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("size", [9, 11, 13])
+def test_rows_with_outlier_channels(cuda, m, size):
+    # one channel 2^size times the others.  (A small softmax_scale: what the two
+    # parts leave out of the other channels, 2^-17 of the outlier, is bounded by
+    # sums of absolute values, of little use for scores of 10.)
+    lens = [m + 200, m]
+    st, table = filled(lens, 2, 32, m, bad=False)
+    q = normal(m + 1, 8, 2 * m, 128)
+    q[..., 5] *= 2.0 ** size
+    check(q, st, table, lens, [m, m], 2.0 ** -(size - 2) if m < MANY else 2.0 ** -size, f"{m} {size}", split=m >= MANY)
