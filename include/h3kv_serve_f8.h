@@ -61,7 +61,9 @@ typedef struct {
   int32_t head_dim; /* must be 128 */
 } h3kv_paged_store_f8;
 
-/* Bytes of the four buffers together (0 for invalid arguments). */
+/* Bytes of the four buffers together (0 for invalid arguments, and for a store that
+ * the calls refuse: more than 65535 heads, or pages * kv_heads * page_size above
+ * 2^31 - 256). */
 size_t h3kv_paged_store_f8_bytes(int32_t pages, int32_t kv_heads, int32_t page_size, int32_t head_dim);
 
 /* Append the rows cu_new[i] .. cu_new[i+1]-1 of K and V (bf16 [kv_heads, n, 128])
@@ -91,7 +93,8 @@ h3kv_status h3kv_paged_append_f8(const h3kv_rows *Q, int32_t q_heads, const h3kv
 h3kv_status h3kv_paged_read_f8(const h3kv_paged_store_f8 *store, const int32_t *rows, int64_t n, const h3kv_rows *K,
                                const h3kv_rows *V, void *stream);
 
-/* h3kv_paged_copy of these pages. */
+/* h3kv_paged_copy of these pages; n is at most 2^27 - 16, and less where a page's
+ * codes of all heads take more than 128 KB: n * 2 * (16 KB pieces of them) < 2^31. */
 h3kv_status h3kv_paged_copy_f8(const h3kv_paged_store_f8 *store, const int32_t *src, const int32_t *dst, int64_t n,
                                void *stream);
 

@@ -345,7 +345,6 @@ __global__ void __launch_bounds__(kThreads)
 // A page's codes of all heads are contiguous, and so are its scales: chunks of
 // 16 KB, one CTA each; the first of K and of V takes the scales along.  1500 pages of
 // 64 rows and 8 heads 61 us, 6.5 TB/s.
-constexpr int kCopyChunk = 16384;
 __global__ void __launch_bounds__(kThreads)
     copy_kernel(const PagedF8Args p, const int32_t *__restrict__ src, const int32_t *__restrict__ dst,
                 const uint32_t chunks) {
@@ -436,11 +435,9 @@ cudaError_t launch_read_f8(const PagedF8Args &p, const int32_t *rows, int64_t n,
 
 cudaError_t launch_copy_f8(const PagedF8Args &p, const int32_t *src, const int32_t *dst, int64_t n,
                            cudaStream_t stream) {
-  const int64_t bytes = (static_cast<int64_t>(p.kv_heads) << p.page_shift) * 128;
-  const int64_t chunks = (bytes + kCopyChunk - 1) / kCopyChunk;
-  if (n > INT32_MAX / (2 * chunks)) return cudaErrorInvalidValue;
-  copy_kernel<<<static_cast<unsigned>(n * 2 * chunks), kThreads, 0, stream>>>(p, src, dst,
-                                                                            static_cast<uint32_t>(chunks));
+  const int64_t blocks = copy_f8_blocks(p);
+  copy_kernel<<<static_cast<unsigned>(n * blocks), kThreads, 0, stream>>>(p, src, dst,
+                                                                        static_cast<uint32_t>(blocks / 2));
   return cudaGetLastError();
 }
 

@@ -41,6 +41,12 @@ cudaError_t launch_append_f8(const PagedF8Args &p, const RotateArgs &r, const Ba
                              cudaStream_t stream);
 cudaError_t launch_read_f8(const PagedF8Args &p, const int32_t *rows, int64_t n, const h3kv_rows &K,
                            const h3kv_rows &V, const ServeDevice &d, cudaStream_t stream);
+// Blocks that copy a page: chunks of 16 KB of its codes of K and of V.
+constexpr int kCopyChunk = 16384;
+inline int64_t copy_f8_blocks(const PagedF8Args &p) {
+  const int64_t bytes = (static_cast<int64_t>(p.kv_heads) << p.page_shift) * 128;
+  return 2 * ((bytes + kCopyChunk - 1) / kCopyChunk);
+}
 cudaError_t launch_copy_f8(const PagedF8Args &p, const int32_t *src, const int32_t *dst, int64_t n,
                            cudaStream_t stream);
 

@@ -16,14 +16,17 @@ using h3kv::Span;
 using h3kv::span;
 using namespace h3kv::checks;
 
+// Sizes that a store may have: row numbers, and rows of all heads, in 31 bits.
+bool store_sizes_ok(int32_t pages, int32_t kv_heads, int32_t page_size) {
+  return pages >= 0 && kv_heads >= 0 && kv_heads <= kMaxHeads && page_shift_of(page_size) &&
+         static_cast<int64_t>(pages) * page_size <= kMaxRows / (kv_heads > 0 ? kv_heads : 1);
+}
+
 h3kv_status paged_f8_args(const h3kv_paged_store_f8 *st, PagedF8Args *out) {
   if (!st || st->pages < 0 || st->kv_heads < 0 || st->kv_heads > kMaxHeads) return H3KV_ERR_INVALID_ARG;
   if (st->head_dim != H3KV_HEAD_DIM) return H3KV_ERR_UNSUPPORTED;
   const int32_t ps = st->page_size;
-  if (!page_shift_of(ps)) return H3KV_ERR_INVALID_ARG;
-  // row numbers, and rows of all heads, in 31 bits
-  if (static_cast<int64_t>(st->pages) * ps > kMaxRows / (st->kv_heads > 0 ? st->kv_heads : 1))
-    return H3KV_ERR_INVALID_ARG;
+  if (!store_sizes_ok(st->pages, st->kv_heads, ps)) return H3KV_ERR_INVALID_ARG;
   if (st->pages > 0 && st->kv_heads > 0) {
     if (!st->k_codes || !st->v_codes || !st->k_scales || !st->v_scales) return H3KV_ERR_INVALID_ARG;
     if (!aligned(st->k_codes, 16) || !aligned(st->v_codes, 16) || !aligned(st->k_scales, 16) ||
@@ -145,8 +148,7 @@ h3kv_status h3kv_paged_append_rotated(const h3kv_rows *Q, int32_t q_heads, const
 }
 
 size_t h3kv_paged_store_f8_bytes(int32_t pages, int32_t kv_heads, int32_t page_size, int32_t head_dim) {
-  if (pages < 0 || kv_heads < 0 || head_dim != H3KV_HEAD_DIM || !page_shift_of(page_size)) return 0;
-  if (static_cast<int64_t>(pages) * page_size > kMaxRows) return 0;
+  if (head_dim != H3KV_HEAD_DIM || !store_sizes_ok(pages, kv_heads, page_size)) return 0;
   return static_cast<size_t>(2) * static_cast<size_t>(pages) * static_cast<size_t>(kv_heads) *
          (static_cast<size_t>(page_size) * H3KV_HEAD_DIM + sizeof(float));
 }
@@ -203,6 +205,7 @@ h3kv_status h3kv_paged_copy_f8(const h3kv_paged_store_f8 *store, const int32_t *
   if (st != H3KV_OK) return st;
   if (n < 0 || n > kMaxRows / 16) return H3KV_ERR_INVALID_ARG;
   if (n == 0 || p.kv_heads == 0) return H3KV_OK;
+  if (n > INT32_MAX / h3kv::copy_f8_blocks(p)) return H3KV_ERR_INVALID_ARG;  // a launch's blocks
   if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return H3KV_ERR_INVALID_ARG;
   const StoreSpans of = store_spans(p);
   if (of.meets(span(src, 4 * n)) || of.meets(span(dst, 4 * n))) return H3KV_ERR_INVALID_ARG;
