@@ -52,30 +52,35 @@ __device__ __forceinline__ void rotate_q(const PagedF8Args &p, const RotateArgs 
   }
 }
 
-// One warp writes the new rows of one sequence and head of K or of V, page by
-// page: once over the page's rows for the largest value, once for the codes.  Bound
-// by latency: one token each of 1 to 64 sequences, 32 and 8 heads, 3.4 - 4 us, of 256
-// 6.2.  (16 rows at once, loads and angles of all of them under way, took registers for
-// 170 a thread: 28 us.)
+// New rows of a sequence and of a head of K (pair 2 h) or of V (2 h + 1), from token `lo`
+// on: of that token's page, or all where they are no more than a page's.
+struct NewRows {
+  int32_t seq, lo;  // seq -1: none
+  int32_t c0, m, len;
+  uint32_t pair;
+};
+
+// One warp writes them, page by page: once over the page's rows for the largest value, once
+// for the codes.  (16 rows at once, loads and angles of all of them under way, took
+// registers for 170 a thread: 28 us.)
 template <int kMode, bool kKeys>
-__device__ __forceinline__ void append_rows(const PagedF8Args &p, const RotateArgs &r, const BatchArgs &b, int i, int h) {
-  const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
-  const BatchCounts c = batch_counts(b, p.page_shift, r.n, i);
-  if (c.bad && h == 0 && kKeys && lane == 0) atomicOr(p.err, kErrIndex);
-  const int32_t p0 = c.len - c.m;
+__device__ __forceinline__ void append_pages(const PagedF8Args &p, const RotateArgs &r, const BatchArgs &b,
+                                             const NewRows &c) {
+  const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3, h = c.pair >> 1;
+  const int32_t p0 = c.len - c.m, end = c.m <= p.page_size ? c.len : min(c.len, (c.lo & ~(p.page_size - 1)) + p.page_size);
   uint8_t *codes = kKeys ? p.k_codes : p.v_codes;
   float *scales = kKeys ? p.k_scales : p.v_scales;
   const h3kv_rows &in = kKeys ? r.k : r.v;
-  for (int32_t lo = p0, hi; lo < c.len; lo = hi) {
+  for (int32_t lo = c.lo, hi; lo < end; lo = hi) {
     const int32_t begin = lo & ~(p.page_size - 1);
-    hi = min(begin + p.page_size, c.len);
-    const int32_t page = batch_page(b, p, i, lo);
+    hi = min(begin + p.page_size, end);
+    const int32_t page = batch_page(b, p, c.seq, lo);
     const int64_t at = static_cast<int64_t>(page) * p.kv_heads + h;
     uint8_t *base = codes + (at << p.page_shift) * 128;
     float y[16];
     auto get = [&](int32_t j) {
       const int32_t pos = min(j, hi - 1);
-      const int64_t t = c.c0 + (pos - p0);
+      const int64_t t = static_cast<int64_t>(c.c0) + (pos - p0);
       const uint4 *src = row_at(in, h, t, l);
       const uint4 a = src[0], z = src[8];
       if constexpr (kKeys && kMode != kRotNone) {
@@ -88,6 +93,7 @@ __device__ __forceinline__ void append_rows(const PagedF8Args &p, const RotateAr
       }
     };
     float top = 0.f;
+#pragma unroll 1
     for (int32_t j = lo; j < hi; j += 4) {
       get(j + sub);
 #pragma unroll
@@ -109,6 +115,7 @@ __device__ __forceinline__ void append_rows(const PagedF8Args &p, const RotateAr
       }
     }
     const float m = exp2i(-e);
+#pragma unroll 1
     for (int32_t j = lo; j < hi; j += 4) {
       if (hi - lo > 4) get(j + sub);  // (up to 4 rows are still there)
       __syncwarp();  // (K_out may be K: every lane's part of the row has been read)
@@ -119,7 +126,7 @@ __device__ __forceinline__ void append_rows(const PagedF8Args &p, const RotateAr
           dst[8] = f8_codes8(y + 8, m);
         }
         if (kKeys && r.k_out.data) {
-          uint4 *dst = row_out(r.k_out, h, c.c0 + (j + sub - p0), l);
+          uint4 *dst = row_out(r.k_out, h, static_cast<int64_t>(c.c0) + (j + sub - p0), l);
           dst[0] = pack_bf16x8(y);
           dst[8] = pack_bf16x8(y + 8);
         }
@@ -130,18 +137,91 @@ __device__ __forceinline__ void append_rows(const PagedF8Args &p, const RotateAr
   }
 }
 
-template <int kMode>
-__global__ void __launch_bounds__(kThreads)
-    append_few_kernel(const PagedF8Args p, const RotateArgs r, const BatchArgs b, const int64_t kv_units) {
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (w < kv_units) {
-    const int64_t u = w >> 1;
-    const int i = static_cast<int>(u / p.kv_heads), h = static_cast<int>(u - static_cast<int64_t>(i) * p.kv_heads);
-    if (w & 1) append_rows<kMode, false>(p, r, b, i, h);
-    else append_rows<kMode, true>(p, r, b, i, h);
-  } else if constexpr (kMode != kRotNone) {
-    if ((w - kv_units) * 4 < r.n * r.q_heads) rotate_q<kMode>(p, r, b, w - kv_units);
+// What the blocks of append_few_kernel do: `first` of them begin the new rows of each
+// sequence, a warp for each head of K or of V; `later` take the pages behind a sequence's
+// first where it has more new tokens than a page; the rest rotate Q.  A page depends
+// on nothing in the pages before it, so that a chunk beside single tokens is not one
+// warp's work: 63 tokens and a chunk of 2048, 32 and 8 heads, 41 us (875 so), 127 and one
+// of 8192 71 us (3878), 31 and one of 512 39 us (224).
+//
+// Places of later pages: from 2 cu[i] >> shift on for sequence i.  One of m tokens, more
+// than a page's, has at most (m - 2 >> shift) + 1 such pages, which is no more than the
+// 2 m >> shift places that it has at least.  A lane each of a block's first warp looks for
+// the page at one of `span` places, by bisection; the warps share those that there are.
+// (Counts that fall, which is reported, may hide pages of other sequences.)
+struct FewBlocks {
+  uint32_t first, later;
+  int32_t span;
+};
+
+// The page at a place.
+__device__ __forceinline__ NewRows later_page(const PagedF8Args &p, const BatchArgs &b, int64_t n, int64_t place) {
+  auto begin = [&](int i) { return 2 * static_cast<int64_t>(__ldg(b.cu + i)) >> p.page_shift; };
+  int lo = 0, hi = b.seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (begin(mid) <= place) lo = mid;
+    else hi = mid;
   }
+  const int64_t k = place - begin(lo);
+  const BatchCounts c = batch_counts(b, p.page_shift, n, lo);
+  const int64_t at = (((c.len - c.m) >> p.page_shift) + 1 + k) << p.page_shift;
+  const bool on = k >= 0 && c.m > p.page_size && at < c.len;
+  return {on ? lo : -1, static_cast<int32_t>(at), static_cast<int32_t>(c.c0), c.m, c.len, 0};
+}
+
+// A block's share of the later pages.  A function of its own: inlined, it took the
+// registers of the kernel from 64 to 84, and 4096 single tokens 72 us for 66.
+template <int kMode>
+__device__ __noinline__ void append_later(const PagedF8Args &p, const RotateArgs &r, const BatchArgs &b, uint32_t x,
+                                          int32_t span) {
+  __shared__ NewRows pages[32];
+  __shared__ int found;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const uint32_t pairs = 2 * p.kv_heads, group = x / pairs;
+    NewRows page = {-1};
+    if (lane < span) page = later_page(p, b, r.n, static_cast<int64_t>(group) * span + lane);
+    page.pair = x - group * pairs;
+    const uint32_t on = __ballot_sync(0xffffffffu, page.seq >= 0);
+    if (page.seq >= 0) pages[__popc(on & ((1u << lane) - 1))] = page;
+    if (lane == 0) found = __popc(on);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = warp; k < found; k += kWarps) {
+    if (pages[k].pair & 1) append_pages<kMode, false>(p, r, b, pages[k]);
+    else append_pages<kMode, true>(p, r, b, pages[k]);
+  }
+}
+
+// Bound by latency: one token each of 1 to 64 sequences, 32 and 8 heads, 3.4 - 4 us, of 256
+// 6.8.  Blocks an SM, by the registers of a rotation's angles and partners.
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, kMode == kRotNone || kMode == kRotHalves128 ? 4 : 2)
+    append_few_kernel(const __grid_constant__ PagedF8Args p, const __grid_constant__ RotateArgs r,
+                      const __grid_constant__ BatchArgs b, const FewBlocks blocks) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= blocks.first + blocks.later) {
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - blocks.first - blocks.later) * kWarps + warp;
+    if constexpr (kMode != kRotNone) {
+      if (unit * 4 < r.n * r.q_heads) rotate_q<kMode>(p, r, b, unit);
+    }
+    return;
+  }
+  if (blockIdx.x >= blocks.first) {
+    append_later<kMode>(p, r, b, blockIdx.x - blocks.first, blocks.span);
+    return;
+  }
+  const uint32_t pairs = 2 * p.kv_heads;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp, i = w / pairs;
+  if (i >= b.seqs) return;
+  const BatchCounts c = batch_counts(b, p.page_shift, r.n, static_cast<int>(i));
+  const NewRows page = {static_cast<int32_t>(i), c.len - c.m, static_cast<int32_t>(c.c0), c.m, c.len,
+                        static_cast<uint32_t>(w - i * pairs)};
+  if (c.bad && page.pair == 0 && lane == 0) atomicOr(p.err, kErrIndex);
+  if (page.pair & 1) append_pages<kMode, false>(p, r, b, page);
+  else append_pages<kMode, true>(p, r, b, page);
 }
 
 // Many new tokens: a block takes windows of kTokens positions of a sequence, whole
@@ -383,16 +463,30 @@ __global__ void __launch_bounds__(kThreads)
 
 namespace {
 
+// The blocks of append_few_kernel.  A block's warps have a place each while that takes no
+// more than four blocks an SM.
+FewBlocks few_blocks(const PagedF8Args &p, const BatchArgs &b, int64_t n, int32_t num_sms) {
+  const int64_t pairs = 2 * static_cast<int64_t>(p.kv_heads), places = (2 * n >> p.page_shift) + 1;
+  FewBlocks f = {};
+  f.first = static_cast<uint32_t>((b.seqs * pairs + kWarps - 1) / kWarps);
+  for (f.span = kWarps; f.span < 32 && (places + f.span - 1) / f.span * pairs > 4 * num_sms;) f.span *= 2;
+  if (n > p.page_size) f.later = static_cast<uint32_t>((places + f.span - 1) / f.span * pairs);
+  return f;
+}
+
 // Which of the two kernels is sooner done, by what they take (32 and 8 heads, pages
-// of 64): a warp of the one for few goes through a sequence's tokens in 0.42 us each
-// behind a start of 3.5, all warps through 6600 rows of K, V and Q a microsecond; a
-// block of the other takes 1.5 us a step where windows are full, 2.5 where they are
-// not, behind 6 us.  Measured, tokens of each sequence, few and many: 1 x 4 3.6 and
-// 5.6, 1 x 12 7.9 and 6.0, 1 x 64 30 and 7.5; 16 x 12 7.7 and 13, 16 x 64 31 and
-// 19; 64 x 16 10 and 38, 64 x 64 36 and 41; 256 x 1 6 and 44, 256 x 64 115 and 108.
-bool many_tokens(int64_t n, int64_t seqs, int64_t steps, int64_t window, int64_t blocks) {
+// of 64): a warp of the one for few goes through a page's tokens, or a short sequence's, in
+// 0.42 us each behind a start of 3.5, and through as many pages as its group of places
+// has for each warp; all warps through 6600 rows of K, V and Q a microsecond; a block
+// of the other takes 1.5 us a step where windows are full, 2.5 where they are not, behind
+// 6 us.  Measured, tokens of each sequence, few and many: 1 x 4 3.6 and 5.6, 1 x 12 7.9 and
+// 6.0, 1 x 64 30 and 7.5; 16 x 12 7.7 and 13, 16 x 64 31 and 19 (pages of 16: 14.5 and
+// 18); 64 x 16 10 and 38, 64 x 64 36 and 41; 256 x 1 6 and 44, 256 x 64 115 and 108.
+// The host knows no more than the mean: where single tokens hide a chunk, its pages take the
+// one for few up to a whole page's time (39 us for 31 tokens and a chunk of 512).
+bool many_tokens(int64_t n, int64_t seqs, int64_t steps, int64_t page, int64_t window, int64_t blocks) {
   const double mean = static_cast<double>(n) / seqs, rows = static_cast<double>(n) * steps;
-  const double alone = 3.5 + 0.42 * mean, all = 2.5 + rows / 6600, few = alone > all ? alone : all;
+  const double alone = 3.5 + 0.42 * (mean < page ? mean : page), all = 2.5 + rows / 6600, few = alone > all ? alone : all;
   const double per_block = (static_cast<double>(n) / window + seqs) * steps / blocks;
   return few > 6.0 + (mean >= window ? 1.5 : 2.5) * per_block;
 }
@@ -401,16 +495,16 @@ template <int kMode>
 cudaError_t launch_append(const PagedF8Args &p, const RotateArgs &r, const BatchArgs &b, const ServeDevice &d,
                           cudaStream_t stream) {
   const int window = p.page_size <= 64 ? 64 : 128, blocks = d.num_sms * (window == 64 && kMode != kRotHalves ? 2 : 1);
-  if (many_tokens(r.n, b.seqs, 2 * p.kv_heads + r.q_heads, window, blocks)) {
+  const FewBlocks f = few_blocks(p, b, r.n, d.num_sms);
+  if (many_tokens(r.n, b.seqs, 2 * p.kv_heads + r.q_heads, p.page_size * f.span / kWarps, window, blocks)) {
     if (window == 64) append_many_kernel<kMode, 64><<<blocks, 512, 0, stream>>>(p, r, b);
     else append_many_kernel<kMode, 128><<<blocks, 1024, 0, stream>>>(p, r, b);
     return cudaGetLastError();
   }
-  const int64_t kv_units = static_cast<int64_t>(b.seqs) * p.kv_heads * 2;
-  const int64_t units = kv_units + (kMode != kRotNone ? (r.n * r.q_heads + 3) / 4 : 0);
-  const int64_t grid = (units + kWarps - 1) / kWarps;
+  const int64_t q_units = kMode != kRotNone ? (r.n * r.q_heads + 3) / 4 : 0;
+  const int64_t grid = f.first + static_cast<int64_t>(f.later) + (q_units + kWarps - 1) / kWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  append_few_kernel<kMode><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p, r, b, kv_units);
+  append_few_kernel<kMode><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p, r, b, f);
   return cudaGetLastError();
 }
 }  // namespace
