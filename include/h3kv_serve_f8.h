@@ -116,7 +116,7 @@ size_t h3kv_attend_paged_f8_workspace_bytes(int32_t q_heads, int32_t kv_heads, i
  *   values; weights rounded to fp16 for the second product (down to 2^-32 of the
  *   largest), fp32 sums;  softmax_scale and lse as h3kv_attend_tree.
  * A query row is taken times a power of two.  For few rows as fp16, exact for
- * elements down to 2^-31 of the row's largest and within 2^-39 of that below; for
+ * elements down to 2^-32 of the row's largest and within 2^-40 of that below; for
  * many as the sum of two e4m3 parts, exact down to 2^-9 of the largest and within
  * 2^-17 of that below, or within 2^-76 (a row with channels far above the rest keeps
  * fewer bits of these).  A row of Q with an element beyond 65504, an infinity or NaN

@@ -95,10 +95,11 @@ __device__ __forceinline__ uint32_t scale2(uint32_t x, uint32_t s) {
 }
 
 // q' = fp16(q H) of a row in place, by 8 lanes (l: the lane among them).  e4m3: q' = q
-// 2^-e, with the row's largest element in [2^14, 2^15): fp16 holds a bf16 element whose
-// last bit is 2^-24 or more there, exactly (down to 2^-31 of the largest), and any
-// other to half of that, 2^-39 of the largest.  c2 2^e, which the row's scores are
-// multiplied with beside K's scale, goes to `factor`.  (fp16(q) loses what lies below
+// 2^-e, with the row's largest element in [2^15, 2^16): fp16 holds a bf16 element whose
+// last bit is 2^-24 or more there, exactly (down to 2^-32 of the largest), and any
+// other to half of that, 2^-40 of the largest.  c2 2^e, which the row's scores are
+// multiplied with beside K's scale, goes to `factor`; e is at most 0 for elements up to
+// 65504, so that the factor is an fp32 number where c2 is.  (fp16(q) loses what lies below
 // 2^-17, whatever the row's size.)
 template <bool kF8>
 __device__ __forceinline__ void rotate_row(uint16_t (&row)[kQPitch], int l, float c2, float *factor) {
@@ -113,7 +114,7 @@ __device__ __forceinline__ void rotate_row(uint16_t (&row)[kQPitch], int l, floa
 #pragma unroll
     for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     // (kept where 2^-e is an fp32 number)
-    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 141, -100);
+    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 142, -100);
     const float m = __int_as_float((127 - e) << 23);
 #pragma unroll
     for (int k = 0; k < 16; ++k) v[k] *= m;

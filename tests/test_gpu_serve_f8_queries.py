@@ -75,3 +75,40 @@ def test_rows_with_outlier_channels(cuda, m, size):
     q = normal(m + 1, 8, 2 * m, 128)
     q[..., 5] *= 2.0 ** size
     check(q, st, table, lens, [m, m], 2.0 ** -(size - 2) if m < MANY else 2.0 ** -size, f"{m} {size}", split=m >= MANY)
+
+
+@pytest.mark.parametrize("m", ROWS)
+def test_factors_next_to_the_largest(cuda, m):
+    # a row of 65280, the largest bf16 that fp16 holds, a softmax_scale next to
+    # fp32's end: the keys whose least code gives a score share a row, zeros have none
+    n, ps = m + 200, 32
+    pages = -(-n // ps)
+    st = b.PagedStoreF8.empty(pages, 1, ps)
+    v = normal(m, 1, pages * ps, 128)
+    table = i32(range(pages)).view(1, pages)
+    b.paged_append_f8(v.to(DEV), v.to(DEV), st, table, i32([pages * ps]), i32([0, pages * ps]))
+    some = np.random.default_rng(m).random(pages * ps) < 0.3
+    some[0] = True
+    st.k_codes.view(torch.uint8).zero_()
+    st.k_codes.view(torch.uint8).view(-1, 128)[torch.from_numpy(some).to(DEV), 7] = 1  # 2^-9
+    st.k_scales.fill_(2.0 ** -15)
+    q = torch.zeros((4, m, 128))
+    q[..., 7] = 65280.0
+    q[3, :, 7] = -65280.0
+    scale = 1.4e38
+    lse = torch.zeros((4, m), device=DEV)
+    o = b.attend_paged_f8(q.to(torch.bfloat16).to(DEV), st, table, i32([n]), i32([0, m]), scale, lse=lse)
+    b.sync_status()
+    vals = so.gather(st.v_codes.view(torch.uint8).cpu().numpy(), st.v_scales.double().cpu().numpy(), list(range(pages)), n)[0]
+    see = np.arange(n)[None, :] <= n - m + np.arange(m)[:, None]
+    score = 65280.0 * 2.0 ** -24 * scale
+    for h in range(4):
+        w = (see & (some[:n] if h < 3 else ~some[:n])[None, :]).astype(float)
+        count = w.sum(1)
+        w /= count[:, None]
+        # weights of exactly one, an fp32 sum of as many values, a divide, a rounding to bf16
+        off = (count + 16)[:, None] * 2.0 ** -23 * (w @ np.abs(vals)) + 2.0 ** -8 * np.abs(w @ vals) * (1 + 2.0 ** -7)
+        within(o[h], w @ vals, off, f"head {h}")
+        want = score if h < 3 else 0.0
+        got = lse[h].cpu().double().numpy()
+        assert (np.abs(got - want - np.log(count)) <= 2.0 ** -20 * want + 1e-4).all(), h
