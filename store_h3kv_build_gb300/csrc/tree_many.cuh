@@ -8,9 +8,9 @@
 // share: 1.9 us for 256 rows over a 128-key tile, where the products alone take
 // 1.3 (the tensor rate) and the bytes 0.75.  A segment costs some 12 us more
 // before its first tile (counts, query rows, first page) and 4 behind its last.
-// A thread spills 56 bytes.  Measured at 64 nodes, 32 query heads over 8: 2 x
-// 131072 cached rows 228 us (1207 TFLOP/s), 32 x 8192 250 us, 128 x 2048 334 us,
-// 512 x 512 506 us.
+// A thread spills 56 bytes (e4m3: 92).  Measured at 64 nodes, 32 query heads over 8: 2 x
+// 131072 cached rows 228 us (1207 TFLOP/s), 32 x 8192 247 us, 128 x 2048 315 us,
+// 512 x 512 453 us; 16 over 4 heads: 133, 138, 176 and 244 us.
 //
 // e4m3: K's codes go to the products as they are (kind::f8f6f4), with a row of Q as the
 // sum of two e4m3 parts, which costs QK what fp16 does; V's are dequantised.  A tile
@@ -202,7 +202,7 @@ __device__ __forceinline__ float split_row(const float (&v)[16], uint2 (&hi)[2],
 // the rows' scales to `scales`.  Zeros behind the segment's rows, up to the end of a
 // softmax warp's 32.  8 lanes hold a row (values 8l .. 8l+7 and 64 + 8l .. of it).
 // Four warps take 4 rows each in turn (kStep 16), so that few rows are shared evenly
-// (drafts 52.7 -> 50.7 us), or 32 rows each (4), which full tiles do as well with.
+// (e4m3 drafts 52.7 -> 50.7 us), or 32 rows each (4), which full tiles do as well with.
 // Loops that are not unrolled: instructions that run once a segment are waited for
 // (unrolled, this took 10 us; e4m3, 8 rows at a time, 4 lanes each, 230 instructions for
 // 150: drafts 53.4 for 52.5 us).  A segment's first scores wait for this: stream 1's
@@ -730,10 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(smem_u32(&sm.q_free[q]), q_phase[q], w))) break;
         load_rows<kF8, kStep>(a, s, sm.q[q], (s.two ? q * kBM : 0) + dw * kEach, dw * kEach);
       }
-      // (stream 1's rows come while stream 0's are rotated)
-#pragma unroll 1
-      for (int q = first || !ok ? 2 : 0; q < 2; ++q) {
-        if (!has_tiles(s, q)) continue;
+      // (stream 1's rows come while stream 0's are rotated.  kvi8r: unrolled, with which 64
+      // nodes of 32 heads over 8 take 228 us on 2 x 131072 rows and 315 on 128 x 2048; 242 and
+      // 335 as a loop, where the compiler spills more.  e4m3: 64 rows over 128 x 1024 120 us
+      // as a loop, 127 unrolled.)
+#pragma unroll(kF8 ? 1 : 2)
+      for (int q = 0; q < 2; ++q) {
+        if (first || !ok || !has_tiles(s, q)) continue;
         if (q == 0 && has_tiles(s, 1)) copy16_wait_but<1>();
         else copy16_wait();
         rotate_rows<kF8, kStep>(s.rows, sm.q[q], sm.qs[kF8 ? sr.r.slot : 0][q], (s.two ? q * kBM : 0) + dw * kEach,
