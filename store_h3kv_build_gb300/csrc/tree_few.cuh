@@ -61,13 +61,13 @@ struct FewSmem {
     float page_scale[kStages][2][kBN / 16];  // e4m3: of K's and V's runs of 16 keys
   };
   uint16_t q[TreeSegs::kDepth][8 * kNT][kQPitch];  // q' of a segment's rows, by its slot
-  float factor[kF8 ? TreeSegs::kDepth : 1][kF8 ? 8 * kNT : 1];  // e4m3: of their scores
   float m[kWarps][8 * kNT], l[kWarps][8 * kNT];
   uint64_t path[TreeSegs::kDepth][8 * kNT];  // e4m3: the keys that the row sees
   uint64_t full[kStages], empty[kStages], q_full[TreeSegs::kDepth];
   Scan scan;
   TreeSegs segs;
   int abort;
+  alignas(8) float factor[kF8 ? TreeSegs::kDepth : 1][kF8 ? 8 * kNT : 1];  // e4m3: of the rows' scores
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -333,9 +333,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // the step's codes and scales into registers, and the stage is free again
       uint4 kw[2][2], vw[4];
       uint32_t k0, k1, v0, v1;
-      // what the scores of rows 8 nt + 2 i4 + {0, 1} are multiplied with (read behind the
-      // products, e4m3 items of 16 rows took 2 % longer; kept for all tiles, too)
-      float2 ck[kNT];
+      // e4m3: what the scores of rows 8 nt + 2 i4 + {0, 1} are multiplied with (read behind
+      // the products, items of 16 rows took 2 % longer; kept for all tiles, too).  kvi8r: c2
+      // (held here as well, items of 32 rows took 4 % longer).
+      float2 ck[kF8 ? kNT : 1];
       auto load_v = [&] {
         const uint8_t *vb = sm.v[r.slot] + v_row;
 #pragma unroll
@@ -372,8 +373,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         } else {
           k0 = sm.ks[r.slot][key0 + g8] * 0x10001u;
           k1 = sm.ks[r.slot][key0 + g8 + 8] * 0x10001u;
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) ck[nt] = make_float2(c2, c2);
         }
       }
       if (!kBig || pos >= keys) load_v();
@@ -449,7 +448,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st[nt][e] = (st[nt][e] + su[nt][e]) * (e & 1 ? ck[nt].y : ck[nt].x);
+          for (int e = 0; e < 4; ++e)
+            st[nt][e] = (st[nt][e] + su[nt][e]) * (!kF8 ? c2 : e & 1 ? ck[kF8 ? nt : 0].y : ck[kF8 ? nt : 0].x);
         }
         if (pos + 16 > base_key) {
           const int32_t n0 = pos + g8 - base_key, n1 = n0 + 8;
