@@ -131,8 +131,8 @@ __device__ __forceinline__ void rotate_row(uint16_t (&row)[kQPitch], int l, floa
 
 // Items of 32 rows: O of a thread takes 128 registers, so the consumers get 224,
 // the query fragments are read again for each tile and V's codes only behind
-// K's products; 108 bytes a thread are spilled all the same (24 with items of
-// 16).  (In two items of 16 rows, 8 nodes of four heads over 32 x 8192
+// K's products; 100 bytes a thread are spilled all the same (24 with items of
+// 16; e4m3: 156 and 20).  (In two items of 16 rows, 8 nodes of four heads over 32 x 8192
 // rows took 234 us; 161 so.)
 constexpr uint32_t kRegConsumer = 224, kRegOther = 56;
 static_assert(2 * kRegConsumer + kRegOther == 3 * 168, "register split");
