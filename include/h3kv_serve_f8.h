@@ -84,8 +84,8 @@ size_t h3kv_paged_store_f8_bytes(int32_t pages, int32_t kv_heads, int32_t page_s
  * beyond 448 * 2^7 and infinities are held as that, NaN as NaN.  A tensor's rows
  * of no sequence are not read, and nothing is written for them.  (Where cu_new
  * falls, which is reported, new tokens of other sequences may be left out.)  A call may
- * mix single tokens with long chunks: it takes the time of the tokens of a page or
- * two, one after the other, beyond that of the bytes. */
+ * mix single tokens with long chunks: it takes the time of the tokens of one to four
+ * pages, one after the other, beyond that of the bytes. */
 h3kv_status h3kv_paged_append_f8(const h3kv_rows *Q, int32_t q_heads, const h3kv_rows *Q_out, const h3kv_rows *K,
                                  const h3kv_rows *V, const h3kv_rows *K_out, const h3kv_rotation *rotation,
                                  const int32_t *positions, int64_t n, const h3kv_paged_store_f8 *store,
